@@ -18,12 +18,12 @@ __all__ = [
     "CSA2Error", "lib", "library_path",
     "csa2_quantize_kv", "csa2_quantize_kv_batch", "quant_job", "QuantJob", "csa2_compress_quantize_kv", "csa2_index_topk", "csa2_index_topk_workspace_size",
     "csa2_index_topk_scored", "csa2_topk_merge_shards", "csa2_topk_merge_shards_workspace_size",
-    "csa2_attn_merge_shards", "csa2_sparse_attn_shard", "csa2_pool_extend",
+    "csa2_attn_merge_shards", "csa2_sparse_attn_shard", "csa2_pool_extend", "csa2_page_maps", "csa2_page_ids",
     "csa2_sparse_attn", "csa2_sparse_attn_workspace_size", "csa2_sparse_attn_plan", "csa2_sparse_attn_noalloc",
     "csa2_layer_group", "csa2_layer_group_workspace_size", "csa2_device_error", "csa2_selftest_bounded_wait",
     "csa2_status_string", "csa2_version", "csa2_launch_count", "GroupDesc", "LayerDesc",
     "csa2_host_alloc", "csa2_host_free", "host_empty",
-    "FMT_FP4", "FMT_FP8_TOKEN", "DTYPE_F32", "DTYPE_BF16", "MODE_FULL", "MODE_REINDEX",
+    "FMT_FP4", "FMT_FP8_TOKEN", "FMT_MXFP4", "DTYPE_F32", "DTYPE_BF16", "MODE_FULL", "MODE_REINDEX",
     "MODE_REUSE", "CSA2_OK", "CSA2_ERR_INVALID_ARG", "CSA2_ERR_SHAPE", "CSA2_ERR_TIMEOUT",
 ]
 
@@ -34,6 +34,7 @@ CSA2_ERR_TIMEOUT = 6
 
 FMT_FP4 = 0
 FMT_FP8_TOKEN = 1
+FMT_MXFP4 = 2
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
 MODE_FULL = 0
@@ -64,7 +65,7 @@ class QuantJob(ctypes.Structure):
 
 
 # the csa2_version() the descriptors and signatures below mirror
-ABI_VERSION = 6
+ABI_VERSION = 7
 
 
 class GroupDesc(ctypes.Structure):
@@ -142,6 +143,11 @@ def lib():
                                   _vp, _vp, _sz, _vp]
     L.csa2_pool_extend.restype = _i32
     L.csa2_pool_extend.argtypes = [_vp, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp]
+    L.csa2_page_maps.restype = _i32
+    L.csa2_page_maps.argtypes = [_vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp,
+                                 _vp, _i64, _vp, _vp, _vp, _i64, _vp]
+    L.csa2_page_ids.restype = _i32
+    L.csa2_page_ids.argtypes = [_vp, _i32, _i32, _i32, _vp, _i32, _i32, _vp, _vp]
     L.csa2_sparse_attn_plan.restype = _i32
     L.csa2_sparse_attn_plan.argtypes = [_i32, _i32, _i32, ctypes.POINTER(_i32), ctypes.POINTER(_i32),
                                         ctypes.POINTER(_i32)]
@@ -329,6 +335,22 @@ def csa2_pool_extend(pool, pool_len, P_in, n_ref, n_entries, q_pos, B, T, P_out,
                      stream=None) -> None:
     _check(lib().csa2_pool_extend(_ptr(pool), _ptr(pool_len), P_in, _ptr(n_ref), _ptr(n_entries), _ptr(q_pos),
                                   B, T, P_out, _ptr(out_pool), _ptr(out_len), _stream(stream)))
+
+
+def csa2_page_maps(old_tokens, new_tokens, B, ratio, page_entries, window, table, max_pages, free_pages, n_free,
+                   free_next, free_next_out, n_entries, swa_len, entry_off, entry_rows, cap_entries, token_off,
+                   window_rows, q_pos, cap_tokens, stream=None) -> None:
+    """Block table, cache rows, window slots and positions of a step's new tokens (see include/csa2.h)."""
+    _check(lib().csa2_page_maps(_ptr(old_tokens), _ptr(new_tokens), B, ratio, page_entries, window, _ptr(table),
+                                max_pages, _ptr(free_pages), n_free, _ptr(free_next), _ptr(free_next_out),
+                                _ptr(n_entries), _ptr(swa_len), _ptr(entry_off), _ptr(entry_rows), cap_entries,
+                                _ptr(token_off), _ptr(window_rows), _ptr(q_pos), cap_tokens, _stream(stream)))
+
+
+def csa2_page_ids(ids, B, T, K, table, max_pages, page_entries, out, stream=None) -> None:
+    """Entry numbers to rows of a paged cache, through each request's block table."""
+    _check(lib().csa2_page_ids(_ptr(ids), B, T, K, _ptr(table), max_pages, page_entries, _ptr(out),
+                               _stream(stream)))
 
 
 def csa2_sparse_attn_plan(rows, H, K):

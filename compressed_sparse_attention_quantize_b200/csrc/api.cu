@@ -18,11 +18,15 @@ cudaError_t launch_attn_merge_shards(const float *, const float *, int, int, int
 cudaError_t launch_selftest_bounded_wait(int, cudaStream_t);
 cudaError_t launch_compress_fp4(const void *, int, int64_t, int, int, int64_t, const float *, int64_t,
                                 uint8_t *, int64_t, uint8_t *, int64_t, const int64_t *, cudaStream_t);
-cudaError_t launch_quant_fp4(const void *, int, int64_t, int, int64_t, uint8_t *, int64_t,
+cudaError_t launch_quant_fp4(int, const void *, int, int64_t, int, int64_t, uint8_t *, int64_t,
                              uint8_t *, int64_t, const int64_t *, cudaStream_t);
 cudaError_t launch_quant_fp8_token(const void *, int, int64_t, int, int64_t, uint8_t *, int64_t,
                                    uint8_t *, int64_t, const int64_t *, cudaStream_t);
 cudaError_t launch_quant_batch(const csa2_quant_job *, int, cudaStream_t);
+cudaError_t launch_page_maps(const int32_t *, const int32_t *, int, int, int, int, int32_t *, int, const int32_t *, int,
+                             const int32_t *, int32_t *, int32_t *, int32_t *, int64_t *, int64_t *, int64_t, int64_t *,
+                             int64_t *, int32_t *, int64_t, cudaStream_t);
+cudaError_t launch_page_ids(const int32_t *, int64_t, int, int, const int32_t *, int, int, int32_t *, cudaStream_t);
 cudaError_t launch_pool_extend(const int32_t *, const int32_t *, int, const int32_t *, const int32_t *,
                                const int32_t *, int, int, int, int32_t *, int32_t *, cudaStream_t);
 }  // namespace csa2
@@ -43,6 +47,7 @@ using namespace csa2;
 namespace {
 
 inline bool aligned16(const void *p) { return (((uintptr_t)p) & 15u) == 0; }
+inline bool aligned_to(const void *p, uintptr_t n) { return (((uintptr_t)p) & (n - 1)) == 0; }
 inline cudaStream_t as_stream(void *s) { return reinterpret_cast<cudaStream_t>(s); }
 thread_local char t_last_error[256] = "";
 inline csa2_status cuda_status(cudaError_t e) {
@@ -137,7 +142,7 @@ const char *csa2_status_string(csa2_status s) {
     return "CSA2: unknown status";
 }
 
-int csa2_version(void) { return 6; }
+int csa2_version(void) { return 7; }
 
 const char *csa2_last_error_string(void) { return t_last_error; }
 
@@ -146,13 +151,18 @@ uint64_t csa2_launch_count(void) { return g_launches.load(std::memory_order_rela
 static csa2_status check_quant_args(int fmt, const void *x, int x_dtype, int64_t rows, int dim,
                                     int64_t x_stride, const uint8_t *codes, int64_t code_stride,
                                     const void *scales, int64_t scale_stride) {
-    if (fmt != CSA2_FMT_FP4_E2M1_E4M3S16 && fmt != CSA2_FMT_FP8_E4M3_TOKEN) return CSA2_ERR_INVALID_ARG;
+    if (fmt != CSA2_FMT_FP4_E2M1_E4M3S16 && fmt != CSA2_FMT_FP8_E4M3_TOKEN && fmt != CSA2_FMT_MXFP4_E2M1_E8M0S32)
+        return CSA2_ERR_INVALID_ARG;
     if (x_dtype != CSA2_DTYPE_F32 && x_dtype != CSA2_DTYPE_BF16) return CSA2_ERR_INVALID_ARG;
     if (rows == 0) return CSA2_OK;                               // no-op, whatever the strides
     if (rows < 0 || dim <= 0 || (dim % 16) || dim > 65536 || x_stride < dim) return CSA2_ERR_SHAPE;
     if (!x || !codes || !scales) return CSA2_ERR_INVALID_ARG;
     if (fmt == CSA2_FMT_FP4_E2M1_E4M3S16) {
         if (code_stride < dim / 2 || scale_stride < dim / 16) return CSA2_ERR_SHAPE;
+        return CSA2_OK;
+    }
+    if (fmt == CSA2_FMT_MXFP4_E2M1_E8M0S32) {
+        if ((dim % 32) || code_stride < dim / 2 || scale_stride < dim / 32) return CSA2_ERR_SHAPE;
         return CSA2_OK;
     }
     if (code_stride < dim || scale_stride < 4) return CSA2_ERR_SHAPE;
@@ -167,8 +177,8 @@ csa2_status csa2_quantize_kv(int fmt, const void *x, int x_dtype, int64_t rows, 
     const csa2_status s = check_quant_args(fmt, x, x_dtype, rows, dim, x_stride, codes, code_stride, scales,
                                            scale_stride);
     if (s != CSA2_OK || rows == 0) return s;
-    if (fmt == CSA2_FMT_FP4_E2M1_E4M3S16)
-        return cuda_status(launch_quant_fp4(x, x_dtype, rows, dim, x_stride, codes, code_stride,
+    if (fmt != CSA2_FMT_FP8_E4M3_TOKEN)
+        return cuda_status(launch_quant_fp4(fmt, x, x_dtype, rows, dim, x_stride, codes, code_stride,
                                             (uint8_t *)scales, scale_stride, dst_rows,
                                             as_stream(stream)));
     return cuda_status(launch_quant_fp8_token(x, x_dtype, rows, dim, x_stride, codes, code_stride,
@@ -300,6 +310,39 @@ csa2_status csa2_pool_extend(const int32_t *pool, const int32_t *pool_len, int P
         return CSA2_ERR_SHAPE;
     return cuda_status(launch_pool_extend(pool, pool_len, P_in, n_ref, n_entries, q_pos, B * T, T, P_out, out_pool,
                                           out_len, as_stream(stream)));
+}
+
+csa2_status csa2_page_maps(const int32_t *old_tokens, const int32_t *new_tokens, int B, int ratio, int page_entries,
+                           int window, int32_t *table, int max_pages, const int32_t *free_pages, int n_free,
+                           const int32_t *free_next, int32_t *free_next_out, int32_t *n_entries, int32_t *swa_len,
+                           int64_t *entry_off, int64_t *entry_rows, int64_t cap_entries, int64_t *token_off,
+                           int64_t *window_rows, int32_t *q_pos, int64_t cap_tokens, void *stream) {
+    const Range range("csa2_page_maps");
+    if (B < 1 || B > CSA2_MAX_REQUESTS || ratio < 1 || page_entries < 1 || page_entries > (1 << 20) || window < 1 ||
+        window > (1 << 20) || max_pages < 1 || n_free < 0 || cap_entries < 0 || cap_tokens < 0)
+        return CSA2_ERR_SHAPE;
+    if (!old_tokens || !new_tokens || !table || (!free_pages && n_free > 0) || !free_next || !free_next_out ||
+        free_next == free_next_out || !n_entries || !entry_off || (!entry_rows && cap_entries > 0) || !token_off)
+        return CSA2_ERR_INVALID_ARG;
+    if (!aligned_to(old_tokens, 4) || !aligned_to(new_tokens, 4) || !aligned_to(table, 4) || !aligned_to(free_pages, 4) ||
+        !aligned_to(free_next, 4) || !aligned_to(free_next_out, 4) || !aligned_to(n_entries, 4) ||
+        !aligned_to(swa_len, 4) || !aligned_to(entry_off, 8) || !aligned_to(entry_rows, 8) || !aligned_to(token_off, 8) ||
+        !aligned_to(window_rows, 8) || !aligned_to(q_pos, 4))
+        return CSA2_ERR_ALIGN;
+    return cuda_status(launch_page_maps(old_tokens, new_tokens, B, ratio, page_entries, window, table, max_pages, free_pages,
+                                        n_free, free_next, free_next_out, n_entries, swa_len, entry_off, entry_rows,
+                                        cap_entries, token_off, window_rows, q_pos, cap_tokens, as_stream(stream)));
+}
+
+csa2_status csa2_page_ids(const int32_t *ids, int B, int T, int K, const int32_t *table, int max_pages,
+                          int page_entries, int32_t *out, void *stream) {
+    const Range range("csa2_page_ids");
+    if (!ids || !table || !out) return CSA2_ERR_INVALID_ARG;
+    if (B < 1 || T < 1 || (int64_t)B * T > (1 << 30) || K < 1 || max_pages < 1 || page_entries < 1 ||
+        page_entries > (1 << 20))
+        return CSA2_ERR_SHAPE;
+    if (!aligned_to(ids, 4) || !aligned_to(table, 4) || !aligned_to(out, 4)) return CSA2_ERR_ALIGN;
+    return cuda_status(launch_page_ids(ids, (int64_t)B * T, T, K, table, max_pages, page_entries, out, as_stream(stream)));
 }
 
 csa2_status csa2_attn_merge_shards(const float *outs, const float *lses, int G, int rows, int H, int D,

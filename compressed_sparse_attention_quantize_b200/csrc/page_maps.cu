@@ -1,0 +1,336 @@
+// Block tables and slot maps of a step, built on the GPU from the requests' lengths, and the
+// translation of entry numbers to cache rows through a block table.
+//
+// Request b holds old[b] tokens and gets new[b] - old[b] more; every `ratio` tokens make one cache
+// entry; a page holds E entries.  With e0 = old / ratio, e1 = new / ratio, the request has
+// ceil(e0 / E) pages and needs ceil(e1 / E).  New pages come from the free list in request order:
+// request b's first new page is the list's entry next + sum of the needs of requests before b.
+//
+// page_maps_kernel: one launch.  Every CTA repeats the exclusive scans over the requests (tokens,
+// entries, pages) into shared memory: at most 4096 requests are a few loads per thread, while
+// handing the scans from one CTA to the others would cost a second launch (about 2 us more than the
+// whole call takes for a decode step).  The maps' places are then spread over the CTAs, four
+// tokens or two entries to a thread, each thread finding its first request by a binary search in
+// shared memory.  No CTA reads what another writes: a new entry's page comes from the free list
+// itself, not from the table, and the list's position is read from one word and written to another.
+// Bound: the maps' bytes (12 per token place, 8 per entry place) for long prefill steps, launch
+// latency for a decode step.
+#include "common.cuh"
+
+namespace csa2 {
+namespace pm {
+
+constexpr int kThreads = 256;
+constexpr int kTok = 4;                  // token places per thread: a 16-byte store of positions
+constexpr int kEnt = 2;                  // entry places per thread: a 16-byte store of rows
+
+struct Args {
+    const int32_t *old_tokens, *new_tokens;
+    int B, ratio, E, window;
+    int32_t *table;
+    int max_pages;
+    const int32_t *free_pages;
+    int n_free;
+    const int32_t *free_next;
+    int32_t *free_next_out;
+    int32_t *n_entries, *swa_len;
+    int64_t *entry_off, *entry_rows;
+    int64_t cap_entries;
+    int64_t *token_off, *window_rows;
+    int32_t *q_pos;
+    int64_t cap_tokens;
+    bool vec;                            // 16-byte stores: the maps' bases allow them
+};
+
+// A request's lengths as the kernel uses them.
+struct Lens {
+    int32_t o, n;                        // tokens before and after the step
+    int64_t e0, e1;                      // entries before and after
+    int64_t have, need;                  // pages held, pages to take (both within the table's width)
+    bool bad;
+};
+CSA2_D Lens lens_of(const Args &a, int b) {
+    Lens l;
+    const int32_t o = a.old_tokens[b], n = a.new_tokens[b];
+    l.bad = o < 0 || n < o;
+    l.o = max(o, 0);
+    l.n = max(n, l.o);
+    l.e0 = l.o / a.ratio;
+    l.e1 = l.n / a.ratio;
+    const int64_t have = (l.e0 + a.E - 1) / a.E, want = (l.e1 + a.E - 1) / a.E;
+    l.bad |= want > a.max_pages;
+    l.have = min(have, (int64_t)a.max_pages);
+    l.need = min(want, (int64_t)a.max_pages) - l.have;
+    return l;
+}
+
+// Last index i with off[i] <= x (off ascending, off[0] <= x).
+CSA2_D int find_request(const int64_t *off, int B, int64_t x) {
+    int lo = 0, hi = B;                  // off[lo] <= x; off[hi] > x or hi == B
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (off[mid] <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+CSA2_D int64_t warp_scan(int64_t v, int lane) {          // inclusive
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += o;
+    }
+    return v;
+}
+
+__global__ void __launch_bounds__(kThreads) page_maps_kernel(const Args a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int B = a.B, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    int64_t *tok = reinterpret_cast<int64_t *>(smem);     // [B + 1] token offsets
+    int64_t *ent = tok + B + 1;                           // [B + 1] entry offsets
+    int64_t *pag = ent + B + 1;                           // [B + 1] page offsets (needs before b)
+    __shared__ int64_t part[3][kThreads / 32];
+
+    // ---- exclusive scans over the requests: consecutive requests per thread ----
+    const int per = (B + kThreads - 1) / kThreads;
+    const int b0 = min(t * per, B), b1 = min(b0 + per, B);
+    int64_t s[3] = {0, 0, 0};
+    for (int b = b0; b < b1; ++b) {
+        const Lens l = lens_of(a, b);
+        s[0] += l.n - l.o;
+        s[1] += l.e1 - l.e0;
+        s[2] += l.need;
+    }
+    int64_t x[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        x[k] = warp_scan(s[k], lane);
+        if (lane == 31) part[k][warp] = x[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        int64_t before = 0;
+        for (int w = 0; w < warp; ++w) before += part[k][w];
+        x[k] += before - s[k];
+    }
+    for (int b = b0; b < b1; ++b) {
+        const Lens l = lens_of(a, b);
+        tok[b] = x[0];
+        ent[b] = x[1];
+        pag[b] = x[2];
+        x[0] += l.n - l.o;
+        x[1] += l.e1 - l.e0;
+        x[2] += l.need;
+    }
+    if (b1 == B && b0 < B) { tok[B] = x[0]; ent[B] = x[1]; pag[B] = x[2]; }
+    __syncthreads();
+
+    // pages left in the list, from its position on
+    const int32_t next = a.free_next[0];
+    const bool next_ok = next >= 0 && next <= a.n_free;
+    const int64_t avail = next_ok ? a.n_free - next : 0;
+    const int32_t *fresh = a.free_pages + (next_ok ? next : 0);
+
+    // ---- per request: a warp each ----
+    const int nwarps = gridDim.x * (kThreads / 32);
+    for (int b = blockIdx.x * (kThreads / 32) + warp; b < B; b += nwarps) {
+        const Lens l = lens_of(a, b);
+        const int64_t got = min(max(avail - pag[b], (int64_t)0), l.need);
+        for (int64_t k = lane; k < l.need; k += 32)
+            a.table[(int64_t)b * a.max_pages + l.have + k] = k < got ? fresh[pag[b] + k] : -1;
+        if (lane == 0) {
+            if (l.bad || got < l.need) raise_device_error(CSA2_ERR_SHAPE);
+            a.n_entries[b] = (int32_t)min(l.e1, (l.have + got) * a.E);
+            if (a.swa_len) a.swa_len[b] = min(l.n, a.window);
+            a.token_off[b] = tok[b];
+            a.entry_off[b] = ent[b];
+        }
+    }
+    if (blockIdx.x == 0 && t == 0) {
+        a.token_off[B] = tok[B];
+        a.entry_off[B] = ent[B];
+        a.free_next_out[0] = next_ok ? next + (int32_t)min(pag[B], avail) : next;
+        if (!next_ok || tok[B] > a.cap_tokens || ent[B] > a.cap_entries) raise_device_error(CSA2_ERR_SHAPE);
+    }
+
+    // ---- the maps' places ----
+    const int64_t ent_groups = (a.cap_entries + kEnt - 1) / kEnt;
+    const int64_t tok_groups = (a.window_rows || a.q_pos) ? (a.cap_tokens + kTok - 1) / kTok : 0;
+    for (int64_t g = (int64_t)blockIdx.x * kThreads + t; g < ent_groups + tok_groups;
+         g += (int64_t)gridDim.x * kThreads) {
+        if (g < ent_groups) {
+            const int64_t i0 = g * kEnt;
+            int64_t row[kEnt];
+            int b = i0 < ent[B] ? find_request(ent, B, i0) : B;
+#pragma unroll
+            for (int k = 0; k < kEnt; ++k) {
+                const int64_t i = i0 + k;
+                row[k] = -1;
+                if (i >= ent[B] || i >= a.cap_entries) continue;
+                while (i >= ent[b + 1]) ++b;
+                const Lens l = lens_of(a, b);
+                const int64_t e = l.e0 + (i - ent[b]);
+                const int64_t pi = e / a.E;
+                int32_t page = -1;
+                if (pi < l.have)
+                    page = a.table[(int64_t)b * a.max_pages + pi];     // held before this step
+                else if (pi - l.have < min(max(avail - pag[b], (int64_t)0), l.need))
+                    page = fresh[pag[b] + (pi - l.have)];
+                if (page >= 0)
+                    row[k] = (int64_t)page * a.E + (e - pi * a.E);
+                else
+                    raise_device_error(CSA2_ERR_SHAPE);
+            }
+            if (a.vec && i0 + kEnt <= a.cap_entries) {
+                *reinterpret_cast<longlong2 *>(a.entry_rows + i0) = make_longlong2(row[0], row[1]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < kEnt; ++k)
+                    if (i0 + k < a.cap_entries) a.entry_rows[i0 + k] = row[k];
+            }
+            continue;
+        }
+        const int64_t i0 = (g - ent_groups) * kTok;
+        int64_t row[kTok];
+        int32_t pos[kTok];
+        int b = i0 < tok[B] ? find_request(tok, B, i0) : B;
+        int64_t lo = 0, hi = 0;                           // places of request b
+        int32_t o = 0, n = 0;
+#pragma unroll
+        for (int k = 0; k < kTok; ++k) {
+            const int64_t i = i0 + k;
+            row[k] = -1;
+            pos[k] = -1;
+            if (i >= tok[B]) continue;
+            if (i >= hi) {                                // the first place, or a new request begins
+                while (i >= tok[b + 1]) ++b;
+                lo = tok[b];
+                hi = tok[b + 1];
+                const Lens l = lens_of(a, b);
+                o = l.o;
+                n = l.n;
+            }
+            const int32_t p = o + (int32_t)(i - lo);
+            pos[k] = p;
+            // a longer step writes its last `window` tokens: earlier ones would share their slots
+            if (p >= n - a.window) row[k] = (int64_t)b * a.window + p % a.window;
+        }
+        if (a.vec && i0 + kTok <= a.cap_tokens) {
+            if (a.window_rows) {
+                longlong2 *w = reinterpret_cast<longlong2 *>(a.window_rows + i0);
+                w[0] = make_longlong2(row[0], row[1]);
+                w[1] = make_longlong2(row[2], row[3]);
+            }
+            if (a.q_pos) *reinterpret_cast<int4 *>(a.q_pos + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kTok; ++k)
+                if (i0 + k < a.cap_tokens) {
+                    if (a.window_rows) a.window_rows[i0 + k] = row[k];
+                    if (a.q_pos) a.q_pos[i0 + k] = pos[k];
+                }
+        }
+    }
+}
+
+// ---- entry numbers to rows -------------------------------------------------------------------
+// Division of 0 <= n < 2^31 by d >= 1 with a multiplication: for d > 1 and s = ceil(log2 d) - 1,
+// magic = ceil(2^(32+s) / d) < 2^32 has n * (magic * d - 2^(32+s)) < n * 2^(s+1) <= 2^(32+s), so
+// floor(n * magic / 2^(32+s)) is the quotient (the rounded-up reciprocal of Granlund and
+// Montgomery, "Division by invariant integers using multiplication", 1994).
+struct Div {
+    uint32_t d, magic;
+    int shift;
+};
+inline Div make_div(uint32_t d) {
+    Div v{d, 0u, 0};
+    if (d > 1) {
+        int s = 0;
+        while ((2ull << s) < d) ++s;                      // 2^s < d <= 2^(s+1)
+        v.shift = s;
+        v.magic = (uint32_t)(((1ull << (32 + s)) + d - 1) / d);
+    }
+    return v;
+}
+CSA2_D uint32_t div_by(uint32_t n, const Div &v) { return v.d == 1u ? n : __umulhi(n, v.magic) >> v.shift; }
+
+struct IdArgs {
+    const int32_t *ids;
+    int T, K;
+    const int32_t *table;
+    int max_pages;
+    Div E;
+    int32_t *out;
+    bool vec;
+};
+
+CSA2_D int32_t id_to_row(const IdArgs &a, const int32_t *pages, int32_t id) {
+    if (id < 0) return -1;
+    const uint32_t p = div_by((uint32_t)id, a.E);
+    const int32_t page = p < (uint32_t)a.max_pages ? __ldg(pages + p) : -1;
+    const int64_t row = (int64_t)page * a.E.d + ((uint32_t)id - p * a.E.d);
+    if (page < 0 || row > INT32_MAX) {
+        raise_device_error(CSA2_ERR_INVALID_ARG);
+        return -1;
+    }
+    return (int32_t)row;
+}
+
+// blockIdx.y strides over the query rows, blockIdx.x over a row's ids (four to a thread).  Bound by
+// memory: 4 bytes in, 4 out per id; a sequence's table is read through L1.
+__global__ void __launch_bounds__(kThreads) page_ids_kernel(const IdArgs a, int64_t rows) {
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+        const int32_t *pages = a.table + (r / a.T) * a.max_pages;
+        const int32_t *in = a.ids + r * a.K;
+        int32_t *out = a.out + r * a.K;
+        for (int i = (blockIdx.x * kThreads + threadIdx.x) * 4; i < a.K; i += gridDim.x * kThreads * 4) {
+            if (a.vec) {
+                const int4 v = *reinterpret_cast<const int4 *>(in + i);
+                *reinterpret_cast<int4 *>(out + i) = make_int4(id_to_row(a, pages, v.x), id_to_row(a, pages, v.y),
+                                                              id_to_row(a, pages, v.z), id_to_row(a, pages, v.w));
+            } else {
+                for (int k = i; k < min(i + 4, a.K); ++k) out[k] = id_to_row(a, pages, in[k]);
+            }
+        }
+    }
+}
+
+}  // namespace pm
+
+static SmemLimit g_page_maps_smem;
+
+cudaError_t launch_page_maps(const int32_t *old_tokens, const int32_t *new_tokens, int B, int ratio, int E, int window,
+                             int32_t *table, int max_pages, const int32_t *free_pages, int n_free,
+                             const int32_t *free_next, int32_t *free_next_out, int32_t *n_entries, int32_t *swa_len,
+                             int64_t *entry_off, int64_t *entry_rows, int64_t cap_entries, int64_t *token_off,
+                             int64_t *window_rows, int32_t *q_pos, int64_t cap_tokens, cudaStream_t st) {
+    const uintptr_t bases = reinterpret_cast<uintptr_t>(entry_rows) | reinterpret_cast<uintptr_t>(window_rows) |
+                            reinterpret_cast<uintptr_t>(q_pos);
+    pm::Args a{old_tokens, new_tokens, B, ratio, E, window, table, max_pages, free_pages, n_free, free_next,
+               free_next_out, n_entries, swa_len, entry_off, entry_rows, cap_entries, token_off, window_rows, q_pos,
+               cap_tokens, (bases & 15u) == 0};
+    const int smem = 3 * (B + 1) * 8;
+    cudaError_t e = ensure_smem_limit(g_page_maps_smem, pm::page_maps_kernel, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t groups = ceil_div(cap_entries, pm::kEnt) + (window_rows || q_pos ? ceil_div(cap_tokens, pm::kTok) : 0);
+    int64_t blocks = ceil_div(groups, pm::kThreads);
+    const int64_t most = (int64_t)device_sm_count() * 4;
+    blocks = blocks < 1 ? 1 : (blocks > most ? most : blocks);
+    pm::page_maps_kernel<<<(unsigned)blocks, pm::kThreads, smem, st>>>(a);
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_page_ids(const int32_t *ids, int64_t rows, int T, int K, const int32_t *table, int max_pages, int E,
+                            int32_t *out, cudaStream_t st) {
+    const uintptr_t bases = reinterpret_cast<uintptr_t>(ids) | reinterpret_cast<uintptr_t>(out);
+    pm::IdArgs a{ids, T, K, table, max_pages, pm::make_div((uint32_t)E), out, (bases & 15u) == 0 && (K & 3) == 0};
+    const int per_row = (int)ceil_div(K, pm::kThreads * 4);
+    const int64_t y = rows < 65535 ? rows : 65535;
+    pm::page_ids_kernel<<<dim3((unsigned)per_row, (unsigned)y), pm::kThreads, 0, st>>>(a, rows);
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace csa2

@@ -16,6 +16,13 @@
 //    fp32 ulps off) is rounded, and the one midpoint mu it may have crossed is tested exactly:
 //    the sign of |x| - mu*s, one fma, rounded once, is the sign of the exact difference (s and
 //    |x| first scaled by a power of two that brings s into [2^-100, 2^100]).
+//  * Microscaled FP4 (E2M1 with one E8M0 scale per 32 channels, the OCP microscaling format): the
+//    scale is 2^(floor(log2 amax) - 2), taken from amax's exponent bits; mu * 2^e is exact (it
+//    needs two more bits than a subnormal scale 2^-127 has below it), so the same comparisons
+//    decide on the exact quotient.
+// Every kernel skips a row whose destination is negative: the unused end of a row map.
+#include <algorithm>
+
 #include "common.cuh"
 
 namespace csa2 {
@@ -67,24 +74,119 @@ CSA2_D void quantize_block16(const float (&v)[16], uint8_t *cd, uint8_t *sd) {
     *sd = (uint8_t)sc;
 }
 
-// One thread per 16-channel block.
+// Scale byte of a microscaled block from the largest |x| of the block as fp32 bits: the biased
+// exponent less 2, i.e. 2^(floor(log2 amax) - 2) with E2M1's largest exponent 2, at least 2^-127.
+// A block that holds an infinity or a NaN gets the NaN scale 0xFF.
+CSA2_D uint32_t e8m0_scale_byte(uint32_t amax_bits) {
+    const uint32_t e = amax_bits >> 23;
+    return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
+}
+CSA2_D float e8m0_to_f32(uint32_t b) {          // b < 255; byte 0 is the subnormal 2^-127
+    return __uint_as_float(b == 0u ? 0x00400000u : b << 23);
+}
+
+// Channels i .. i+7 of x (element offset i); vec: 16-byte loads.
 template <typename T>
-__global__ void quant_fp4_kernel(const T *__restrict__ x, int64_t rows, int dim, int64_t x_stride,
-                                 uint8_t *__restrict__ codes, int64_t code_stride,
-                                 uint8_t *__restrict__ scales, int64_t scale_stride,
-                                 const int64_t *__restrict__ dst_rows) {
-    const int nblk = dim >> 4;
-    const int64_t total = rows * nblk;
-    for (int64_t t = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; t < total;
-         t += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t r = t / nblk;
-        const int b = (int)(t - r * nblk);
-        const T *xr = x + r * x_stride + b * 16;
-        float v[16];
+CSA2_D void load8(const T *x, bool vec, float (&v)[8]) {
+    if (sizeof(T) == 4) {
+        const float *p = reinterpret_cast<const float *>(x);
+        if (vec) {
+            const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
+            const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = load_as_f32<T>(xr + i);
-        const int64_t d = dst_rows ? dst_rows[r] : r;
-        quantize_block16(v, codes + d * code_stride + b * 8, scales + d * scale_stride + b);
+            for (int k = 0; k < 8; ++k) v[k] = __ldg(p + k);
+        }
+    } else {
+        const uint16_t *p = reinterpret_cast<const uint16_t *>(x);
+        if (vec) {
+            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[2 * k] = __uint_as_float(w[k] << 16);
+                v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = bf16_bits_to_f32(__ldg(p + k));
+        }
+    }
+}
+
+// The codes of 8 neighbouring channels (channel k in bits 4k..) and their block's scale byte; the
+// block's 2 (E4M3 / 16 channels) or 4 (E8M0 / 32 channels) lanes call together.
+template <int FMT>
+CSA2_D uint32_t quantize_lane8(const float (&v)[8], uint32_t &scale) {
+    uint32_t top = 0u;                                   // |x| as bits: ordered, and NaN above all
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+    float s;
+    if (FMT == CSA2_FMT_MXFP4_E2M1_E8M0S32) {
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        scale = e8m0_scale_byte(top);
+        s = scale == 255u ? 0.0f : e8m0_to_f32(scale);
+    } else {
+        // as fmaxf over the block: a NaN takes no part
+        float amax = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(v[k]));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        scale = e4m3_code_mag_rne(__fdiv_rn(amax, 6.0f));
+        s = e4m3_to_f32(scale);
+    }
+    uint32_t w = 0u;
+    if (s != 0.0f) {
+        const E2M1Cuts t = e2m1_cuts(s);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w |= e2m1_code(v[k], t) << (4 * k);
+    }
+    return w;
+}
+
+// FP4 rows: 8 neighbouring channels per thread, read in 16-byte loads where the rows allow it.
+// Bound by memory: x is read once and 4.25 or 4.5 bits per channel are written.
+template <typename T, int FMT>
+__global__ void __launch_bounds__(256)
+quant_fp4_rows_kernel(const T *__restrict__ x, int64_t rows, int dim, int64_t x_stride,
+                      uint8_t *__restrict__ codes, int64_t code_stride, uint8_t *__restrict__ scales,
+                      int64_t scale_stride, const int64_t *__restrict__ dst_rows, bool vec, bool word) {
+    constexpr int kLanes = FMT == CSA2_FMT_MXFP4_E2M1_E8M0S32 ? 4 : 2;   // lanes of a block
+    const uint32_t per_row = (uint32_t)dim >> 3;
+    const int64_t total = rows * (int64_t)per_row;
+    for (int64_t base = (int64_t)blockIdx.x * 256; base < total; base += (int64_t)gridDim.x * 256) {
+        const int64_t t = base + threadIdx.x;
+        const bool live = t < total;                     // blocks are whole: total is a multiple of kLanes
+        float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        int64_t d = -1;
+        uint32_t c = 0;
+        if (live) {
+            int64_t r;
+            if (total <= 0xFFFFFFFFll) {                 // a 32-bit division where it suffices
+                r = (uint32_t)t / per_row;
+                c = (uint32_t)t - (uint32_t)r * per_row;
+            } else {
+                r = t / per_row;
+                c = (uint32_t)(t - r * per_row);
+            }
+            load8<T>(x + r * x_stride + 8 * (int64_t)c, vec, v);
+            d = dst_rows ? dst_rows[r] : r;
+        }
+        uint32_t sc;
+        const uint32_t w = quantize_lane8<FMT>(v, sc);
+        if (d >= 0) {
+            uint8_t *cd = codes + d * code_stride + 4 * (int64_t)c;
+            if (word) {
+                *reinterpret_cast<uint32_t *>(cd) = w;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) cd[k] = (uint8_t)(w >> (8 * k));
+            }
+            if (c % kLanes == 0) scales[d * scale_stride + c / kLanes] = (uint8_t)sc;
+        }
     }
 }
 
@@ -116,6 +218,7 @@ __global__ void compress_fp4_kernel(const T *__restrict__ x, int64_t entries, in
             }
         }
         const int64_t d = dst_rows ? dst_rows[e] : e;
+        if (d < 0) continue;
         quantize_block16(v, codes + d * code_stride + b * 8, scales + d * scale_stride + b);
     }
 }
@@ -210,6 +313,7 @@ __global__ void quant_fp8_token_kernel(const T *__restrict__ x, int64_t rows, in
          r += warps) {
         const T *xr = x + r * x_stride;
         const int64_t d = dst_rows ? dst_rows[r] : r;
+        if (d < 0) continue;
         fp8_token_row(lane, dim, [&](int i) { return load_as_f32<T>(xr + i); }, codes + d * code_stride,
                       reinterpret_cast<float *>(scales + d * scale_stride));
     }
@@ -303,9 +407,10 @@ __global__ void __launch_bounds__(kQuantThreads) quant_batch_kernel(const __grid
     const int64_t lb = (int64_t)blockIdx.x - J.block_start[j];
     const int lane = threadIdx.x & 31;
     const bool vec = rows_vec_aligned(q);
-    if (q.fmt == CSA2_FMT_FP4_E2M1_E4M3S16) {
-        // thread t: row t / (dim/4), channels 4*(t % (dim/4)) ..; dim/4 is a multiple of 4, so
-        // the 4 lanes of a block are lanes 4k .. 4k+3 of one warp
+    if (q.fmt != CSA2_FMT_FP8_E4M3_TOKEN) {
+        // thread t: row t / (dim/4), channels 4*(t % (dim/4)) ..; dim/4 is a multiple of 4 (8 with
+        // 32-channel blocks), so the 4 (8) lanes of a block are neighbours within one warp
+        const bool mx = q.fmt == CSA2_FMT_MXFP4_E2M1_E8M0S32;
         const int64_t quads = q.dim >> 2;
         const int64_t t = lb * kQuantThreads + threadIdx.x;
         const bool live = t < q.rows * quads;
@@ -318,11 +423,23 @@ __global__ void __launch_bounds__(kQuantThreads) quant_batch_kernel(const __grid
             load4(q.x, q.x_dtype, r * q.x_stride + 4 * c4, vec, v);
             d = q.dst_rows ? __ldg(q.dst_rows + r) : r;
         }
-        float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const uint32_t sc = e4m3_code_mag_rne(__fdiv_rn(amax, 6.0f));
-        const float s = e4m3_to_f32(sc);
+        uint32_t sc;
+        float s;
+        if (mx) {
+            uint32_t top = 0u;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = max(top, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+#pragma unroll
+            for (int off = 1; off <= 4; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+            sc = e8m0_scale_byte(top);
+            s = sc == 255u ? 0.0f : e8m0_to_f32(sc);
+        } else {
+            float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            sc = e4m3_code_mag_rne(__fdiv_rn(amax, 6.0f));
+            s = e4m3_to_f32(sc);
+        }
         uint32_t p = 0u;
         if (s != 0.0f) {
             const E2M1Cuts cuts = e2m1_cuts(s);
@@ -331,10 +448,11 @@ __global__ void __launch_bounds__(kQuantThreads) quant_batch_kernel(const __grid
         }
         // lanes 4k and 4k+2 assemble code words 0 and 1 of the block (channels 0-7, 8-15)
         const uint32_t w = p | (__shfl_down_sync(0xffffffffu, p, 1) << 16);
-        if (live && (c4 & 1) == 0) {
+        if (live && d >= 0 && (c4 & 1) == 0) {
             uint8_t *cd = q.codes + d * q.code_stride + (c4 >> 2) * 8 + (c4 & 2) * 2;
             store4(cd, w, ((reinterpret_cast<uintptr_t>(q.codes) | (uintptr_t)q.code_stride) & 3u) == 0);
-            if ((c4 & 3) == 0) q.scales[d * q.scale_stride + (c4 >> 2)] = (uint8_t)sc;
+            if (mx ? (c4 & 7) == 0 : (c4 & 3) == 0)
+                q.scales[d * q.scale_stride + (mx ? c4 >> 3 : c4 >> 2)] = (uint8_t)sc;
         }
     } else if (q.dim <= kRowMaxDim) {
         const int grp = threadIdx.x / kRowGroup, tr = threadIdx.x % kRowGroup;
@@ -362,7 +480,7 @@ __global__ void __launch_bounds__(kQuantThreads) quant_batch_kernel(const __grid
         amax = fmaxf(fmaxf(ga[0], ga[1]), fmaxf(ga[2], ga[3]));
         const float s = __fdiv_rn(amax, 448.0f);
         const E4M3Row kr = e4m3_row(s);
-        if (live) {
+        if (live && d >= 0) {
             uint8_t *cd = q.codes + d * q.code_stride;
             const bool al = ((reinterpret_cast<uintptr_t>(q.codes) | (uintptr_t)q.code_stride) & 3u) == 0;
 #pragma unroll
@@ -382,6 +500,7 @@ __global__ void __launch_bounds__(kQuantThreads) quant_batch_kernel(const __grid
         if (r >= q.rows) return;                                   // uniform per warp
         const int64_t base = r * q.x_stride;
         const int64_t d = q.dst_rows ? q.dst_rows[r] : r;
+        if (d < 0) return;
         fp8_token_row(lane, q.dim, [&](int i) { return load_elem(q.x, q.x_dtype, base + i); },
                       q.codes + d * q.code_stride, reinterpret_cast<float *>(q.scales + d * q.scale_stride));
     }
@@ -400,7 +519,7 @@ cudaError_t launch_quant_batch(const csa2_quant_job *jobs, int n, cudaStream_t s
         q.scales = reinterpret_cast<uint8_t *>(s.scales); q.scale_stride = s.scale_stride;
         q.dst_rows = s.dst_rows;
         J.block_start[J.n] = blocks;
-        if (s.fmt == CSA2_FMT_FP4_E2M1_E4M3S16)
+        if (s.fmt != CSA2_FMT_FP8_E4M3_TOKEN)
             blocks += ceil_div(s.rows * (s.dim / 4), kQuantThreads);
         else if (s.dim <= kRowMaxDim)
             blocks += ceil_div(s.rows, kQuantThreads / kRowGroup);
@@ -416,20 +535,38 @@ cudaError_t launch_quant_batch(const csa2_quant_job *jobs, int n, cudaStream_t s
     return cudaGetLastError();
 }
 
-cudaError_t launch_quant_fp4(const void *x, int x_dtype, int64_t rows, int dim, int64_t x_stride,
+template <typename T, int FMT>
+static void launch_quant_fp4_rows(const T *x, int64_t rows, int dim, int64_t x_stride, uint8_t *codes,
+                                  int64_t code_stride, uint8_t *scales, int64_t scale_stride,
+                                  const int64_t *dst_rows, cudaStream_t st) {
+    const bool vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (x_stride * (int64_t)sizeof(T)) % 16 == 0;
+    const bool word = ((reinterpret_cast<uintptr_t>(codes) | (uintptr_t)code_stride) & 3u) == 0;
+    const int64_t blocks = std::min<int64_t>(ceil_div(rows * (dim / 8), 256), 148 * 64);
+    quant_fp4_rows_kernel<T, FMT><<<(unsigned)blocks, 256, 0, st>>>(x, rows, dim, x_stride, codes, code_stride, scales,
+                                                                    scale_stride, dst_rows, vec, word);
+}
+
+cudaError_t launch_quant_fp4(int fmt, const void *x, int x_dtype, int64_t rows, int dim, int64_t x_stride,
                              uint8_t *codes, int64_t code_stride, uint8_t *scales,
                              int64_t scale_stride, const int64_t *dst_rows, cudaStream_t st) {
-    const int64_t total = rows * (dim / 16);
-    const int threads = 256;
-    int64_t blocks = ceil_div(total, threads);
-    if (blocks > 148 * 64) blocks = 148 * 64;
-    if (x_dtype == CSA2_DTYPE_F32)
-        quant_fp4_kernel<float><<<(unsigned)blocks, threads, 0, st>>>(
-            (const float *)x, rows, dim, x_stride, codes, code_stride, scales, scale_stride, dst_rows);
-    else
-        quant_fp4_kernel<uint16_t><<<(unsigned)blocks, threads, 0, st>>>(
-            (const uint16_t *)x, rows, dim, x_stride, codes, code_stride, scales, scale_stride,
-            dst_rows);
+    const bool mx = fmt == CSA2_FMT_MXFP4_E2M1_E8M0S32;
+    if (x_dtype == CSA2_DTYPE_F32) {
+        const float *xf = (const float *)x;
+        if (mx)
+            launch_quant_fp4_rows<float, CSA2_FMT_MXFP4_E2M1_E8M0S32>(xf, rows, dim, x_stride, codes, code_stride, scales,
+                                                                      scale_stride, dst_rows, st);
+        else
+            launch_quant_fp4_rows<float, CSA2_FMT_FP4_E2M1_E4M3S16>(xf, rows, dim, x_stride, codes, code_stride, scales,
+                                                                    scale_stride, dst_rows, st);
+    } else {
+        const uint16_t *xh = (const uint16_t *)x;
+        if (mx)
+            launch_quant_fp4_rows<uint16_t, CSA2_FMT_MXFP4_E2M1_E8M0S32>(xh, rows, dim, x_stride, codes, code_stride,
+                                                                         scales, scale_stride, dst_rows, st);
+        else
+            launch_quant_fp4_rows<uint16_t, CSA2_FMT_FP4_E2M1_E4M3S16>(xh, rows, dim, x_stride, codes, code_stride,
+                                                                       scales, scale_stride, dst_rows, st);
+    }
     note_launches(1);
     return cudaGetLastError();
 }

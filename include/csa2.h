@@ -56,6 +56,7 @@ typedef enum csa2_status {
 /* quantised formats */
 #define CSA2_FMT_FP4_E2M1_E4M3S16 0   /* E2M1 codes, one E4M3 scale per 16 channels */
 #define CSA2_FMT_FP8_E4M3_TOKEN   1   /* E4M3 codes, one fp32 scale per row (token) */
+#define CSA2_FMT_MXFP4_E2M1_E8M0S32 2 /* E2M1 codes, one E8M0 scale per 32 channels */
 /* float element types */
 #define CSA2_DTYPE_F32  0
 #define CSA2_DTYPE_BF16 1
@@ -97,12 +98,20 @@ CSA2_API int csa2_version(void);
  *   float at scales + d*scale_stride; code_i = E4M3_rne_satfinite(x_i / s) rounded once
  *   from the exact quotient; s == 0 gives all-zero codes.  dim bytes per row.
  *
+ * fmt == CSA2_FMT_MXFP4_E2M1_E8M0S32 (the OCP microscaling format MXFP4; no page defines it: it is
+ *   for the rows and weights of csa2_fp4_matmul):  per block of 32 channels
+ *       X = 2^max(floor(log2 amax) - 2, -127);  code_i = E2M1_rne_satfinite(x_i / X)
+ *   the scale byte is X's exponent + 127 (0 for a block of zeros, whose codes are +-0); a block
+ *   that holds an infinity or a NaN gets the NaN scale 0xFF and zero codes.  Codes as for the
+ *   first format; dim/32 scale bytes per row; dim must be a multiple of 32.
+ *
  * x: rows x dim elements of x_dtype (CSA2_DTYPE_F32 or CSA2_DTYPE_BF16), row r at
  *    x + r*x_stride elements.  dst_rows: optional int64 [rows] destination rows (a cache
- *    position, or a ring slot of the window); NULL writes row r to row r.
+ *    position, or a ring slot of the window); NULL writes row r to row r.  A row whose
+ *    destination is negative is skipped (the unused end of csa2_page_maps' row maps).
  * Errors: INVALID_ARG (NULL x/codes/scales, unknown fmt or dtype), SHAPE (rows < 0,
- *   dim <= 0 or not a multiple of 16, dim > 65536, x_stride < dim), ALIGN (scales for
- *   FP8 not 4-byte aligned or scale_stride not a multiple of 4), CUDA.
+ *   dim <= 0 or not a multiple of 16 (32 for MXFP4), dim > 65536, x_stride < dim), ALIGN (scales
+ *   for FP8 not 4-byte aligned or scale_stride not a multiple of 4), CUDA.
  * rows == 0 is a no-op returning CSA2_OK (checked after fmt and x_dtype, before the rest).
  * ---------------------------------------------------------------------------------- */
 CSA2_API csa2_status csa2_quantize_kv(int fmt, const void *x, int x_dtype, int64_t rows, int dim,
@@ -152,7 +161,7 @@ CSA2_API csa2_status csa2_quantize_kv_batch(const csa2_quant_job *jobs, int n_jo
  * multiply-add); w == NULL takes the mean, w = 1/m (an IEEE fp32 quotient).  The entry is then
  * quantised exactly as csa2_quantize_kv with CSA2_FMT_FP4_E2M1_E4M3S16 and written to
  * destination row d = dst_rows ? dst_rows[e] : e (dim/2 code bytes at codes + d*code_stride,
- * dim/16 E4M3 scale bytes at scales + d*scale_stride).
+ * dim/16 E4M3 scale bytes at scales + d*scale_stride); an entry with a negative d is skipped.
  *
  * x: entries*m token rows of dim elements of x_dtype (CSA2_DTYPE_F32 or CSA2_DTYPE_BF16), token
  *    row t at x + t*x_stride elements.  w: NULL or fp32 [entries][w_stride] (w_stride >= m).
@@ -473,6 +482,60 @@ CSA2_API csa2_status csa2_sparse_attn_shard(const uint16_t *q, int B, int T, int
 CSA2_API csa2_status csa2_attn_merge_shards(const float *outs, const float *lses, int G, int rows,
                                    int H, int D, void *out, int out_dtype, float *lse,
                                    void *stream);
+
+/* ------------------------------------------------------------------------------------
+ * Paged main KV.  A cache of pages of page_entries rows each; request b's entry e is row
+ * table[b][e / page_entries] * page_entries + e % page_entries.  No page defines these calls: they
+ * build on the GPU what a serving step needs to write to and read from a paged cache.
+ *
+ * csa2_page_maps -- block table, cache rows, window slots and positions of a step's new tokens.
+ *   Request b holds old_tokens[b] tokens before the step and new_tokens[b] after it; every `ratio`
+ *   tokens make one compressed entry (e0 = old / ratio entries before, e1 = new / ratio after).
+ *   Requests take the pages they lack, ceil(e1 / page_entries) - ceil(e0 / page_entries), from
+ *   free_pages[*free_next ..) in request order.  In one launch the call writes
+ *     table [B][max_pages]   the new pages behind request b's held ones (which are only read);
+ *     *free_next_out         *free_next + the pages taken (a word of its own: INVALID_ARG if it is
+ *                            free_next; the next step's free_next);
+ *     n_entries [B]          e1 (fewer if pages are missing, see below);
+ *     swa_len [B]            min(new, window) (or NULL);
+ *     entry_off int64 [B+1], entry_rows int64 [cap_entries]   the cache rows of request b's new
+ *                            entries e0 .. e1 - 1 at entry_off[b] .. entry_off[b+1] - 1: the
+ *                            dst_rows of csa2_quantize_kv and csa2_compress_quantize_kv;
+ *     token_off int64 [B+1], window_rows int64 [cap_tokens]   for new token p of request b the row
+ *                            b*window + p % window of a ring of `window` slots per request, -1 for
+ *                            a token that a later one of the same step would overwrite (or NULL);
+ *     q_pos int32 [cap_tokens]   the tokens' positions p (or NULL).
+ *   Places behind the last request (up to cap_entries, cap_tokens) are set to -1, so a captured
+ *   graph can quantise whole maps: csa2_quantize_kv skips rows with a negative destination.
+ *   Lengths that break the contract (old < 0 or new < old: taken as no new tokens), a free list or
+ *   table width that does not suffice (the missing pages are -1, their rows -1, n_entries counts
+ *   the entries that have a page) and more new tokens or entries than the maps hold record
+ *   CSA2_ERR_SHAPE in the device error word.
+ * Errors: INVALID_ARG (a NULL array other than those marked; entry_rows may be NULL when
+ *   cap_entries is 0 and free_pages when n_free is 0), SHAPE (B < 1 or > CSA2_MAX_REQUESTS, ratio,
+ *   page_entries, window or max_pages < 1, page_entries or window > 2^20, n_free, cap_entries or
+ *   cap_tokens < 0), ALIGN (an int64 array not 8-byte, an int32 array not 4-byte aligned), CUDA.
+ *
+ * csa2_page_ids -- entry numbers to cache rows: out[r][i] = the row of entry ids[r][i] of request
+ *   r / T, -1 where the id is negative.  With these rows as ids and seq_start = 0 csa2_sparse_attn
+ *   reads a paged cache.  ids, out int32 [B*T][K] (out may be ids).  An id beyond the table, on a
+ *   page that is not there (-1) or whose row does not fit int32 gives -1 and records
+ *   CSA2_ERR_INVALID_ARG in the device error word.
+ * Errors: INVALID_ARG (NULL ids, table or out), SHAPE (B, T, K, max_pages or page_entries < 1,
+ *   B*T > 2^30, page_entries > 2^20), ALIGN (ids, table or out not 4-byte aligned), CUDA.
+ * ---------------------------------------------------------------------------------- */
+#define CSA2_MAX_REQUESTS 4096
+
+CSA2_API csa2_status csa2_page_maps(const int32_t *old_tokens, const int32_t *new_tokens, int B, int ratio,
+                                    int page_entries, int window, int32_t *table, int max_pages,
+                                    const int32_t *free_pages, int n_free, const int32_t *free_next,
+                                    int32_t *free_next_out, int32_t *n_entries, int32_t *swa_len,
+                                    int64_t *entry_off, int64_t *entry_rows, int64_t cap_entries,
+                                    int64_t *token_off, int64_t *window_rows, int32_t *q_pos,
+                                    int64_t cap_tokens, void *stream);
+
+CSA2_API csa2_status csa2_page_ids(const int32_t *ids, int B, int T, int K, const int32_t *table, int max_pages,
+                                   int page_entries, int32_t *out, void *stream);
 
 /* ------------------------------------------------------------------------------------
  * csa2_device_error -- reads (and clears) the library's device-side error word for the
