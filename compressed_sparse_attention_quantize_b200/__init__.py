@@ -19,6 +19,7 @@ __all__ = [
     "csa2_quantize_kv", "csa2_quantize_kv_batch", "quant_job", "QuantJob", "csa2_compress_quantize_kv", "csa2_index_topk", "csa2_index_topk_workspace_size",
     "csa2_index_topk_scored", "csa2_topk_merge_shards", "csa2_topk_merge_shards_workspace_size",
     "csa2_attn_merge_shards", "csa2_sparse_attn_shard", "csa2_pool_extend", "csa2_page_maps", "csa2_page_ids",
+    "csa2_fp4_matmul", "csa2_fp4_matmul_workspace_size",
     "csa2_sparse_attn", "csa2_sparse_attn_workspace_size", "csa2_sparse_attn_plan", "csa2_sparse_attn_noalloc",
     "csa2_layer_group", "csa2_layer_group_workspace_size", "csa2_device_error", "csa2_selftest_bounded_wait",
     "csa2_status_string", "csa2_version", "csa2_launch_count", "GroupDesc", "LayerDesc",
@@ -143,6 +144,11 @@ def lib():
                                   _vp, _vp, _sz, _vp]
     L.csa2_pool_extend.restype = _i32
     L.csa2_pool_extend.argtypes = [_vp, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp]
+    L.csa2_fp4_matmul_workspace_size.restype = _i32
+    L.csa2_fp4_matmul_workspace_size.argtypes = [_i64, _i64, _i32, ctypes.POINTER(_sz)]
+    L.csa2_fp4_matmul.restype = _i32
+    L.csa2_fp4_matmul.argtypes = [_i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i32, _f32, _vp,
+                                  _i32, _i64, _vp, _sz, _vp]
     L.csa2_page_maps.restype = _i32
     L.csa2_page_maps.argtypes = [_vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp,
                                  _vp, _i64, _vp, _vp, _vp, _i64, _vp]
@@ -335,6 +341,21 @@ def csa2_pool_extend(pool, pool_len, P_in, n_ref, n_entries, q_pos, B, T, P_out,
                      stream=None) -> None:
     _check(lib().csa2_pool_extend(_ptr(pool), _ptr(pool_len), P_in, _ptr(n_ref), _ptr(n_entries), _ptr(q_pos),
                                   B, T, P_out, _ptr(out_pool), _ptr(out_len), _stream(stream)))
+
+
+def csa2_fp4_matmul_workspace_size(M, N, K) -> int:
+    out = _sz(0)
+    _check(lib().csa2_fp4_matmul_workspace_size(M, N, K, ctypes.byref(out)))
+    return out.value
+
+
+def csa2_fp4_matmul(fmt, a_codes, a_code_stride, a_scales, a_scale_stride, b_codes, b_code_stride, b_scales,
+                    b_scale_stride, M, N, K, alpha, out, out_dtype, out_stride, workspace, ws_bytes,
+                    stream=None) -> None:
+    """out = alpha * a . b^T of two matrices of FP4 rows (see include/csa2.h)."""
+    _check(lib().csa2_fp4_matmul(fmt, _ptr(a_codes), a_code_stride, _ptr(a_scales), a_scale_stride, _ptr(b_codes),
+                                 b_code_stride, _ptr(b_scales), b_scale_stride, M, N, K, alpha, _ptr(out), out_dtype,
+                                 out_stride, _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 def csa2_page_maps(old_tokens, new_tokens, B, ratio, page_entries, window, table, max_pages, free_pages, n_free,

@@ -23,6 +23,9 @@ cudaError_t launch_quant_fp4(int, const void *, int, int64_t, int, int64_t, uint
 cudaError_t launch_quant_fp8_token(const void *, int, int64_t, int, int64_t, uint8_t *, int64_t,
                                    uint8_t *, int64_t, const int64_t *, cudaStream_t);
 cudaError_t launch_quant_batch(const csa2_quant_job *, int, cudaStream_t);
+cudaError_t launch_fp4_matmul(int, const uint8_t *, int64_t, const uint8_t *, int64_t, const uint8_t *, int64_t,
+                              const uint8_t *, int64_t, int64_t, int64_t, int, float, void *, int, int64_t,
+                              cudaStream_t);
 cudaError_t launch_page_maps(const int32_t *, const int32_t *, int, int, int, int, int32_t *, int, const int32_t *, int,
                              const int32_t *, int32_t *, int32_t *, int32_t *, int64_t *, int64_t *, int64_t, int64_t *,
                              int64_t *, int32_t *, int64_t, cudaStream_t);
@@ -310,6 +313,45 @@ csa2_status csa2_pool_extend(const int32_t *pool, const int32_t *pool_len, int P
         return CSA2_ERR_SHAPE;
     return cuda_status(launch_pool_extend(pool, pool_len, P_in, n_ref, n_entries, q_pos, B * T, T, P_out, out_pool,
                                           out_len, as_stream(stream)));
+}
+
+static csa2_status check_matmul_shape(int64_t M, int64_t N, int K) {
+    if (M < 0 || N < 0 || M > INT32_MAX || N > INT32_MAX || K < 1 || K > (1 << 20)) return CSA2_ERR_SHAPE;
+    if (M > 0 && N > (((int64_t)1 << 47) / M)) return CSA2_ERR_SHAPE;
+    return CSA2_OK;
+}
+
+csa2_status csa2_fp4_matmul_workspace_size(int64_t M, int64_t N, int K, size_t *bytes) {
+    if (!bytes) return CSA2_ERR_INVALID_ARG;
+    const csa2_status s = check_matmul_shape(M, N, K);
+    if (s != CSA2_OK) return s;
+    *bytes = kAlign;
+    return CSA2_OK;
+}
+
+csa2_status csa2_fp4_matmul(int fmt, const uint8_t *a_codes, int64_t a_code_stride, const uint8_t *a_scales,
+                            int64_t a_scale_stride, const uint8_t *b_codes, int64_t b_code_stride,
+                            const uint8_t *b_scales, int64_t b_scale_stride, int64_t M, int64_t N, int K,
+                            float alpha, void *out, int out_dtype, int64_t out_stride, void *workspace,
+                            size_t ws_bytes, void *stream) {
+    const Range range("csa2_fp4_matmul");
+    if (fmt != CSA2_FMT_FP4_E2M1_E4M3S16 && fmt != CSA2_FMT_MXFP4_E2M1_E8M0S32) return CSA2_ERR_INVALID_ARG;
+    if (out_dtype != CSA2_DTYPE_F32 && out_dtype != CSA2_DTYPE_BF16) return CSA2_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return CSA2_OK;
+    const csa2_status s = check_matmul_shape(M, N, K);
+    if (s != CSA2_OK) return s;
+    const int block = fmt == CSA2_FMT_FP4_E2M1_E4M3S16 ? 16 : 32;
+    if ((K % block) || a_code_stride < K / 2 || b_code_stride < K / 2 || a_code_stride > ((int64_t)1 << 39) ||
+        b_code_stride > ((int64_t)1 << 39) || a_scale_stride < K / block || b_scale_stride < K / block || out_stride < N)
+        return CSA2_ERR_SHAPE;
+    if (!a_codes || !a_scales || !b_codes || !b_scales || !out) return CSA2_ERR_INVALID_ARG;
+    if (!aligned16(a_codes) || !aligned16(b_codes) || (a_code_stride & 15) || (b_code_stride & 15) ||
+        !aligned_to(out, out_dtype == CSA2_DTYPE_BF16 ? 2 : 4))
+        return CSA2_ERR_ALIGN;
+    if (!workspace || ws_bytes < kAlign) return CSA2_ERR_WORKSPACE;
+    return cuda_status(launch_fp4_matmul(fmt, a_codes, a_code_stride, a_scales, a_scale_stride, b_codes, b_code_stride,
+                                         b_scales, b_scale_stride, M, N, K, alpha, out, out_dtype, out_stride,
+                                         as_stream(stream)));
 }
 
 csa2_status csa2_page_maps(const int32_t *old_tokens, const int32_t *new_tokens, int B, int ratio, int page_entries,

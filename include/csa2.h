@@ -484,6 +484,36 @@ CSA2_API csa2_status csa2_attn_merge_shards(const float *outs, const float *lses
                                    void *stream);
 
 /* ------------------------------------------------------------------------------------
+ * csa2_fp4_matmul -- product of two matrices of FP4 rows, as csa2_quantize_kv leaves them:
+ *     out[m][n] = alpha * sum_k a[m][k] * b[n][k]
+ * with a, b the dequantised values (code times block scale), fp32 accumulation on the tensor
+ * cores, one rounding to out_dtype.  The projections that make queries, latents and indexer rows
+ * from hidden states (no page gives the layer's projection formats; the rows' formats are [B]
+ * section "FP4 量化 + Bounded Replay"'s FP4 and the OCP microscaling MXFP4).
+ *   fmt: CSA2_FMT_FP4_E2M1_E4M3S16 (scale bytes below 0x80: a scale's sign is not read) or
+ *     CSA2_FMT_MXFP4_E2M1_E8M0S32, the same for both.  A NaN scale makes its whole output row
+ *     (column) NaN.
+ *   a: M rows of K codes, row m at a_codes + m*a_code_stride bytes (K/2 bytes), its K/16 (K/32) scale
+ *     bytes at a_scales + m*a_scale_stride; b: N rows likewise (the weights, one row per output
+ *     channel).  out: row m at out + m*out_stride elements.
+ *   workspace: csa2_fp4_matmul_workspace_size bytes (a few: the kernel needs none today).
+ * The result does not depend on timing, but the summation order depends on M, N, K and the device's
+ * SM count, so a row's result may differ in its last fp32 bits between batch sizes.
+ * M == 0 or N == 0 is a no-op returning CSA2_OK (checked after fmt and out_dtype).
+ * Errors: INVALID_ARG (NULL a_codes, a_scales, b_codes, b_scales or out; unknown fmt or out_dtype),
+ *   SHAPE (M or N < 0 or > 2^31 - 1, M * N > 2^47, K < 1, K not a multiple of 16 (32 for MXFP4),
+ *   K > 2^20, code strides < K/2 or > 2^39, scale strides < K/16 (K/32), out_stride < N), ALIGN
+ *   (a_codes, b_codes or their strides not 16-byte aligned, out not aligned to its element),
+ *   WORKSPACE, CUDA.
+ * ---------------------------------------------------------------------------------- */
+CSA2_API csa2_status csa2_fp4_matmul_workspace_size(int64_t M, int64_t N, int K, size_t *bytes);
+CSA2_API csa2_status csa2_fp4_matmul(int fmt, const uint8_t *a_codes, int64_t a_code_stride,
+                                     const uint8_t *a_scales, int64_t a_scale_stride, const uint8_t *b_codes,
+                                     int64_t b_code_stride, const uint8_t *b_scales, int64_t b_scale_stride,
+                                     int64_t M, int64_t N, int K, float alpha, void *out, int out_dtype,
+                                     int64_t out_stride, void *workspace, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------------------
  * Paged main KV.  A cache of pages of page_entries rows each; request b's entry e is row
  * table[b][e / page_entries] * page_entries + e % page_entries.  No page defines these calls: they
  * build on the GPU what a serving step needs to write to and read from a paged cache.
