@@ -9,16 +9,23 @@
 // columns, instead of padding the batch to 128 rows.  Per 256 channels (a stage):
 //   warp 0        the codes of both operands by tensor copies (128-byte rows, 128-byte swizzle; rows
 //                 and channels past the end arrive as zeros)
-//   warps 2-5     the scale bytes, from their rows in global memory to the 512-byte blocks that
-//                 tcgen05.cp reads: byte k of row r at (r % 32) * 16 + (r / 32) * 4 + k, so 128 rows x
-//                 4 scales become 32 lanes x 4 columns.  Scales past the end are zero: a NaN there
-//                 would survive the zero codes.
-//   warp 1        one thread: tcgen05.cp of the stage's scales into TMEM columns of the stage (they
-//                 are rewritten only after the stage's MMAs have completed), then four MMAs
-//                 (kind::mxf4nvf4 with 16-channel, kind::mxf4 with 32-channel scales; K = 64 each)
-//   warps 6-13    epilogue: TMEM -> registers -> global
-// A CTA walks over tiles; the copies and scales of the next tile run while the epilogue drains
-// the last.  Few tiles and a long K are split over a cluster: each CTA takes a run of stages, leaves
+//   warp 2        the scale bytes of four stages at a time (64 or 32 a row) by tensor copies, two such
+//                 chunks in flight.  16 bytes a row and stage through the load units held the whole
+//                 kernel up, each in a cache line of its own (137 us at 4096 x 8192 x 4096).  Rows that
+//                 are not 16-byte aligned come through registers (warps 2-5).  Scales past the end are
+//                 zero: a NaN there would survive the zero codes.
+//   warps 6-9     the scales from shared memory to TMEM: the MMA wants word j (4 scales) of row r in
+//                 lane r % 32, column 4 j + r / 32, repeated in all four lane quarters; each warp writes
+//                 its quarter.  (tcgen05.cp does it from one thread, but queues with the MMAs: 151 us
+//                 for that product with its 12 copies a stage, 54 us without.)
+//   warp 1        one thread: four MMAs a stage (kind::mxf4nvf4 with 16-channel, kind::mxf4 with
+//                 32-channel scales; K = 64 each) into one of two accumulators
+//   warps 10-17   epilogue of the other accumulator: TMEM -> registers -> shared memory -> tensor
+//                 store (direct stores where the output's rows are not 16-byte aligned, or tokens are
+//                 columns)
+// A CTA walks over tiles; everything up to the MMAs of the next tile runs while the epilogue drains
+// the last.  NT = 192 is the widest tile whose two accumulators leave TMEM columns for two stages of
+// scales (2 x 192 + 2 x 48 <= 512).  Few tiles and a long K are split over a cluster: each CTA takes a run of stages, leaves
 // its fp32 tile in its shared memory, and every CTA adds up a share of the columns over the
 // cluster in rank order (no second launch, no atomics: the result does not depend on timing).
 // Every wait is bounded: on expiry the CTA records CSA2_ERR_TIMEOUT, drains, frees TMEM and exits.
@@ -31,38 +38,46 @@ namespace fmm {
 constexpr int kM = 128;                    // left rows per tile
 constexpr int kKTile = 256;                // channels per stage: 128 code bytes a row
 constexpr int kSteps = 4;                  // MMAs per stage (K = 64)
-constexpr int kMaxNT = 256;
-constexpr int kThreads = 448;
-constexpr int kSfThreads = 128;
-constexpr int kEpiThreads = 256;
+constexpr int kMaxNT = 192;
+constexpr int kThreads = 576;
+constexpr int kLoaders = 4;                // scale-loading warps
+constexpr int kChunk = 4;                  // stages of scales loaded at a time
+constexpr int kChunks = 2;                 // such chunks in shared memory
+constexpr int kEpiWarps = 8;
+constexpr int kEpiWarp0 = 10;
 constexpr int kMaxStages = 8;
 constexpr int kMaxSplits = 8;              // portable cluster size
+constexpr int kStoreBytes = 4096;          // a warp's output tile: 32 rows x 128 bytes
 
 struct Operand {
     const uint8_t *scales;
     int64_t scale_stride;
     int64_t rows;
-    bool vec;                              // 16-byte (E4M3) or 8-byte (E8M0) aligned scale rows
 };
 
 struct Args {
     Operand left, right;
     int K, nblk;                           // channels, scale blocks per row
     int NT, stages, splits;
+    int accs, sf_bufs;                     // accumulators, stages of scales in TMEM
     int tiles_l;                           // left tiles
     int64_t tiles;                         // all tiles
     int ktiles;                            // stages of the whole K
     uint32_t tmem_cols, acc_cols;
+    bool sf_tma;                           // both operands' scale rows are 16-byte aligned
     bool swap;                             // left = B: out is written transposed
     float alpha;
     void *out;
     int64_t out_stride;
     bool out_vec;                          // 16-byte stores along n allowed
+    bool out_tma;                          // the epilogue stores tiles by tensor copies
 };
 
 struct Ctl {
-    uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t acc_full, acc_empty, drain;
+    uint64_t full[kMaxStages], empty[kMaxStages];        // the codes are there; the stage is free
+    uint64_t sf_full[kChunks], sf_empty[kChunks];        // chunks of scale bytes in shared memory
+    uint64_t sf_ready[kMaxStages], sf_free[kMaxStages];  // TMEM scale buffers
+    uint64_t acc_full[2], acc_empty[2], drain;
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -85,18 +100,59 @@ CSA2_D void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t
             "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.block16 [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
             ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc) : "memory");
 }
-// 32 rows x 16 bytes of shared memory into 32 lanes x 4 columns of TMEM, repeated for the four
-// lane quarters.
-CSA2_D void cp_scales(uint32_t taddr, uint64_t sdesc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+// 8 consecutive columns of the calling thread's TMEM lane.
+CSA2_D void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
-CSA2_D uint64_t sdesc_scales(uint32_t saddr) {           // no swizzle, 8-row groups 128 bytes apart
-    uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)(16u >> 4) << 16;
-    d |= (uint64_t)(128u >> 4) << 32;
-    d |= (uint64_t)1u << 46;
-    return d;
+// Where 16-byte piece q of row `row` of a chunk is: rows of 64 (E4M3) or 32 (E8M0) bytes, swizzled as
+// the tensor copies write them, so that a warp's reads of one piece from 32 rows meet no conflicts.
+template <int kCells>
+CSA2_D uint32_t chunk_off(int row, int q) {
+    return kCells == 4 ? (uint32_t)(row * 64 + ((q ^ ((row >> 1) & 3)) << 4)) : (uint32_t)(row * 32 + ((q ^ ((row >> 2) & 1)) << 4));
 }
+// Stage i of a chunk of scale rows (kCells words a stage) from shared memory into the columns of the
+// calling warp's lane quarter: per word j the left rows' 4 columns (rows lane, 32 + lane, ..), all
+// left words first, then the right rows' 4 or 8 columns.
+template <int kCells, int kGroups>
+CSA2_D void scales_to_tmem(const uint8_t *ss, int i, int lane, uint32_t taddr) {
+    uint32_t w[1 + kGroups][4][kCells];                  // [group][row quarter][word]
+#pragma unroll
+    for (int g = 0; g <= kGroups; ++g)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int row = g * 128 + c * 32 + lane;
+            if (kCells == 4) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(ss + chunk_off<kCells>(row, i));
+                w[g][c][0] = v.x; w[g][c][1] = v.y; w[g][c][kCells - 2] = v.z; w[g][c][kCells - 1] = v.w;
+            } else {
+                const uint2 v = *reinterpret_cast<const uint2 *>(ss + chunk_off<kCells>(row, i >> 1) + 8 * (i & 1));
+                w[g][c][0] = v.x; w[g][c][1] = v.y;
+            }
+        }
+    uint32_t cols[4 * kCells * (1 + kGroups)];
+#pragma unroll
+    for (int j = 0; j < kCells; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            cols[4 * j + c] = w[0][c][j];
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) cols[4 * (kCells + j * kGroups + g) + c] = w[1 + g][c][j];
+        }
+#pragma unroll
+    for (int q = 0; q < 4 * kCells * (1 + kGroups); q += 8) {
+        const uint32_t v[8] = {cols[q], cols[q + 1], cols[q + 2], cols[q + 3], cols[q + 4], cols[q + 5], cols[q + 6],
+                               cols[q + 7]};
+        tmem_st8(taddr + q, v);
+    }
+}
+CSA2_D void tma_store_2d(const void *tmap, const void *src, int32_t x, int32_t y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+                 ::"l"(tmap), "r"(x), "r"(y), "r"(ptx::smem_u32(src)) : "memory");
+}
+// This thread's bulk stores have read their shared memory.
+CSA2_D void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 CSA2_D void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -109,33 +165,48 @@ CSA2_D float ld_peer(const float *p, uint32_t rank) {
     return v;
 }
 
-// Scale bytes of one row for one stage: 16 (E4M3) or 8 (E8M0), zeros past the row's or the
-// matrix's end.
-template <bool MX>
-CSA2_D uint4 load_scales(const Operand &o, int64_t row, int kt, int nblk) {
-    constexpr int kPer = MX ? 8 : 16;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    const int b0 = kt * kPer;
-    if (row >= o.rows || b0 >= nblk) return v;
-    const uint8_t *p = o.scales + row * o.scale_stride + b0;
-    if (o.vec && b0 + kPer <= nblk) {
-        if (MX) {
-            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
-            v.x = u.x;
-            v.y = u.y;
-        } else {
-            v = __ldg(reinterpret_cast<const uint4 *>(p));
-        }
-    } else {
-        uint32_t w[4] = {0u, 0u, 0u, 0u};
-        const int n = min(kPer, nblk - b0);
+// 16 scale bytes of a row from byte b0 on, for rows without alignment; zeros past the row's or the
+// matrix's end.  Whole aligned words of the scale matrix are read and shifted into place; at the
+// matrix's own ends, where such a word is not all inside, single bytes.
+CSA2_D uint4 load_scales(const Operand &o, int64_t row, int b0, int nblk) {
+    const int n = row < o.rows ? min(16, nblk - b0) : 0;               // bytes that exist
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (n > 0) {
+        const uint8_t *p = o.scales + row * o.scale_stride + b0;
+        const uint8_t *end = o.scales + (o.rows - 1) * o.scale_stride + nblk;
+        const uint32_t sh = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 3u);
+        const uint8_t *q = p - sh;
+        if (q >= o.scales && q + 20 <= end) {
+            uint32_t u[5];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (i < n) w[i >> 2] |= (uint32_t)__ldg(p + i) << (8 * (i & 3));
-        v = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int i = 0; i < 5; ++i) u[i] = __ldg(reinterpret_cast<const uint32_t *>(q) + i);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t v = __funnelshift_r(u[i], u[i + 1], 8u * sh);
+                const int left = n - 4 * i;                            // bytes of this word that exist
+                w[i] = left >= 4 ? v : (left > 0 ? v & ((1u << (8 * left)) - 1u) : 0u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (i < n) w[i >> 2] |= (uint32_t)__ldg(p + i) << (8 * (i & 3));
+        }
     }
-    return v;
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
+
+// A place in the ring of stages: its index and the parity of its round.  (Counters, not i % stages:
+// the divisions of every role's loop took longer than a stage's MMAs.)
+struct Ring {
+    int st = 0;
+    uint32_t ph = 0;
+    CSA2_D void next(int stages) {
+        if (++st == stages) {
+            st = 0;
+            ph ^= 1;
+        }
+    }
+};
 
 struct TileAt {
     int64_t l0, r0;
@@ -144,14 +215,15 @@ CSA2_D TileAt tile_at(const Args &a, int64_t t) {
     return {(t % a.tiles_l) * kM, (t / a.tiles_l) * a.NT};
 }
 
-// 32 consecutive columns (right rows r .. r+31) of left row l.
+// `cols` (32 or 16) consecutive columns (right rows r ..) of left row l.
 template <bool BF16>
-CSA2_D void store_cols(const Args &a, int64_t l, int64_t r, const float (&v)[32]) {
+CSA2_D void store_cols(const Args &a, int64_t l, int64_t r, int cols, const float (&v)[32]) {
     if (l >= a.left.rows) return;
+    const int n = (int)min((int64_t)cols, a.right.rows - r);
     if (a.swap) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            if (r + i >= a.right.rows) break;
+            if (i >= n) break;
             const int64_t at = (r + i) * a.out_stride + l;
             if (BF16)
                 reinterpret_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(v[i]);
@@ -161,7 +233,7 @@ CSA2_D void store_cols(const Args &a, int64_t l, int64_t r, const float (&v)[32]
         return;
     }
     const int64_t at = l * a.out_stride + r;
-    if (a.out_vec && r + 32 <= a.right.rows) {
+    if (a.out_vec && n == 32) {
         if (BF16) {
             uint4 *p = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + at);
 #pragma unroll
@@ -183,7 +255,7 @@ CSA2_D void store_cols(const Args &a, int64_t l, int64_t r, const float (&v)[32]
     }
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-        if (r + i >= a.right.rows) break;
+        if (i >= n) break;
         if (BF16)
             reinterpret_cast<__nv_bfloat16 *>(a.out)[at + i] = __float2bfloat16_rn(v[i]);
         else
@@ -191,31 +263,51 @@ CSA2_D void store_cols(const Args &a, int64_t l, int64_t r, const float (&v)[32]
     }
 }
 
+CSA2_D int code_bytes_of(int NT) { return kM * 128 + ((NT * 128 + 1023) & ~1023); }
+
 template <bool MX, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
-fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const __grid_constant__ CUtensorMap rmap) {
+fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const __grid_constant__ CUtensorMap rmap,
+                  const __grid_constant__ CUtensorMap lsmap, const __grid_constant__ CUtensorMap rsmap,
+                  const __grid_constant__ CUtensorMap omap) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    constexpr int kCells = MX ? 2 : 4;                   // 512-byte scale blocks per 128 rows and stage
+    constexpr int kCells = MX ? 2 : 4;                   // scale words per row and stage
     const int NT = a.NT;
-    const int r_groups = (NT + 127) / 128;               // scale blocks of the right rows
-    const int l_bytes = kM * 128, r_bytes = NT * 128;
-    const int sf_bytes = kCells * 512 * (1 + r_groups);
-    const int stage_bytes = l_bytes + ((r_bytes + 1023) & ~1023) + ((sf_bytes + 1023) & ~1023);
-    Ctl &S = *reinterpret_cast<Ctl *>(base + (size_t)a.stages * stage_bytes);
+    const int r_groups = NT > 128 ? 2 : 1;               // 128-row groups of the right scales
+    const int code_bytes = code_bytes_of(NT);
+    constexpr int kRow = 4 * kCells * kChunk;            // bytes of a scale row in a chunk: 64 or 32
+    const int sf_bytes = kRow * 128 * (1 + r_groups);    // a chunk
+    // the stages' codes, the epilogue warps' output tiles, the chunks of scales, the barriers
+    uint8_t *const store0 = base + (size_t)a.stages * code_bytes;
+    uint8_t *const sf_mem = store0 + (a.out_tma ? kEpiWarps * kStoreBytes : 0);
+    Ctl &S = *reinterpret_cast<Ctl *>(sf_mem + kChunks * sf_bytes);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
 
     const int rank = a.splits > 1 ? (int)(blockIdx.x % a.splits) : 0;
     const int64_t first = blockIdx.x / a.splits, step = gridDim.x / a.splits;
-    const int k0 = (int)((int64_t)a.ktiles * rank / a.splits), k1 = (int)((int64_t)a.ktiles * (rank + 1) / a.splits);
+    // this CTA's stages: runs of whole 16-byte pieces of a scale row (one stage, or two with E8M0)
+    constexpr int kGran = MX ? 2 : 1;
+    const int runs = (a.ktiles + kGran - 1) / kGran;
+    const int k0 = kGran * (runs * rank / a.splits), k1 = min(a.ktiles, kGran * (runs * (rank + 1) / a.splits));
 
     if (t == 0) {
         for (int i = 0; i < a.stages; ++i) {
-            ptx::mbar_init(&S.full[i], 1 + kSfThreads);
+            ptx::mbar_init(&S.full[i], 1);
             ptx::mbar_init(&S.empty[i], 1);
         }
-        ptx::mbar_init(&S.acc_full, 1);
-        ptx::mbar_init(&S.acc_empty, kEpiThreads);
+        for (int i = 0; i < kChunks; ++i) {
+            ptx::mbar_init(&S.sf_full[i], a.sf_tma ? 1 : 32 * kLoaders);
+            ptx::mbar_init(&S.sf_empty[i], 4);
+        }
+        for (int i = 0; i < a.sf_bufs; ++i) {
+            ptx::mbar_init(&S.sf_ready[i], 4);
+            ptx::mbar_init(&S.sf_free[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&S.acc_full[i], 1);
+            ptx::mbar_init(&S.acc_empty[i], kEpiWarps);
+        }
         ptx::mbar_init(&S.drain, 1);
         S.abort_flag = 0;
         ptx::fence_async_smem();
@@ -228,180 +320,259 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = S.tmem_base;
+    const uint32_t sf_col0 = tmem + a.accs * a.acc_cols;
+    const uint32_t sf_cols = (uint32_t)(kCells * 4 * (1 + r_groups));        // per buffer
     volatile int *abort_flag = &S.abort_flag;
 
     if (warp == 0) {
         // ================= codes =================
         if (lane == 0) {
-            int it = 0;
+            Ring p;
+            int held = 0;                                // stages filled since the last full round
             bool ok = true;
             for (int64_t tile = first; ok && tile < a.tiles; tile += step) {
                 const TileAt at = tile_at(a, tile);
-                for (int kt = k0; kt < k1; ++kt, ++it) {
-                    const int st = it % a.stages;
-                    if (it >= a.stages && !ptx::mbar_wait(&S.empty[st], ((it / a.stages) - 1) & 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t *sl = base + (size_t)st * stage_bytes, *sr = sl + l_bytes;
-                    ptx::mbar_arrive_expect_tx(&S.full[st], (uint32_t)(l_bytes + r_bytes));
-                    ptx::tma_load_2d(sl, &lmap, kt * 128, (int32_t)at.l0, &S.full[st]);
-                    ptx::tma_load_2d(sr, &rmap, kt * 128, (int32_t)at.r0, &S.full[st]);
+                for (int kt = k0; kt < k1; ++kt) {
+                    // (the first round's wait for an earlier round returns at once)
+                    if (!ptx::mbar_wait(&S.empty[p.st], p.ph ^ 1, abort_flag)) { ok = false; break; }
+                    uint8_t *sl = base + (size_t)p.st * code_bytes, *sr = sl + kM * 128;
+                    ptx::mbar_arrive_expect_tx(&S.full[p.st], (uint32_t)((kM + NT) * 128));
+                    ptx::tma_load_2d(sl, &lmap, kt * 128, (int32_t)at.l0, &S.full[p.st]);
+                    ptx::tma_load_2d(sr, &rmap, kt * 128, (int32_t)at.r0, &S.full[p.st]);
+                    p.next(a.stages);
+                    held = min(held + 1, a.stages);
                 }
             }
-            // the copies still in flight land before the CTA leaves
-            for (int i = it > a.stages ? it - a.stages : 0; i < it; ++i)
-                ptx::mbar_wait_drain(&S.full[i % a.stages], (i / a.stages) & 1);
+            // the copies still in flight land before the CTA leaves: the last use of each stage
+            for (; held > 0; --held) {
+                if (p.st == 0) { p.st = a.stages; p.ph ^= 1; }
+                --p.st;
+                ptx::mbar_wait_drain(&S.full[p.st], p.ph);
+            }
         }
         __syncwarp();
     } else if (warp == 1) {
         // ================= MMA issuer =================
         if (lane == 0) {
-            const uint32_t sf0 = tmem + a.acc_cols;
-            const uint32_t sf_cols = (uint32_t)(kCells * 4 * (1 + r_groups));   // per stage
-            int it = 0, n = 0;
-            bool ok = true;
-            for (int64_t tile = first; ok && tile < a.tiles; tile += step, ++n) {
-                if (n > 0 && !ptx::mbar_wait(&S.acc_empty, (n - 1) & 1, abort_flag)) break;
+            const uint32_t idesc0 = idesc_fp4(NT, MX, 0), idesc2 = idesc_fp4(NT, MX, 2);
+            const uint64_t da0 = ptx::sdesc_sw128(ptx::smem_u32(base), 16, 1024);
+            const uint32_t stage16 = (uint32_t)code_bytes >> 4, l16 = (kM * 128) >> 4;
+            Ring p, f, acc;
+            bool ok = true, seen = false;                // seen: the next stage was found ready already
+            for (int64_t tile = first; ok && tile < a.tiles; tile += step) {
+                if (!ptx::mbar_wait(&S.acc_empty[acc.st], acc.ph ^ 1, abort_flag)) break;
                 ptx::tc_fence_after();
-                for (int kt = k0; kt < k1; ++kt, ++it) {
-                    const int st = it % a.stages;
-                    if (!ptx::mbar_wait(&S.full[st], (it / a.stages) & 1, abort_flag)) { ok = false; break; }
-                    ptx::tc_fence_after();
-                    const uint32_t sl = ptx::smem_u32(base + (size_t)st * stage_bytes), sr = sl + l_bytes;
-                    const uint32_t ss = sr + ((r_bytes + 1023) & ~1023);
-                    const uint32_t sfa = sf0 + st * sf_cols, sfb = sfa + kCells * 4;
-                    // left blocks one after the other; right blocks of the same channels side by side
-                    for (int c = 0; c < kCells; ++c) {
-                        cp_scales(sfa + 4 * c, sdesc_scales(ss + 512 * c));
-                        for (int g = 0; g < r_groups; ++g)
-                            cp_scales(sfb + 4 * (c * r_groups + g), sdesc_scales(ss + 512 * (kCells * (1 + g) + c)));
+                const uint32_t d = tmem + acc.st * a.acc_cols;
+                for (int kt = k0; kt < k1; ++kt) {
+                    if (!seen && (!ptx::mbar_wait(&S.full[p.st], p.ph, abort_flag) ||
+                                  !ptx::mbar_wait(&S.sf_ready[f.st], f.ph, abort_flag))) {
+                        ok = false;
+                        break;
                     }
-                    const uint64_t da = ptx::sdesc_sw128(sl, 16, 1024), db = ptx::sdesc_sw128(sr, 16, 1024);
+                    ptx::tc_fence_after();
+                    const uint32_t sfa = sf_col0 + f.st * sf_cols, sfb = sfa + kCells * 4;
+                    const uint64_t da = da0 + p.st * stage16, db = da + l16;
+                    const int st = p.st, sb = f.st;
+                    p.next(a.stages);
+                    f.next(a.sf_bufs);
 #pragma unroll
                     for (int k = 0; k < kSteps; ++k) {
-                        const int c = MX ? k >> 1 : k, id = MX ? (k & 1) * 2 : 0;
-                        mma_fp4<MX>(tmem, da + 2 * k, db + 2 * k, idesc_fp4(NT, MX, id), sfa + 4 * c,
+                        // the next stage's barriers are polled while the tensor pipe still has work
+                        if (k == kSteps - 1)
+                            seen = ptx::mbar_test(&S.full[p.st], p.ph) && ptx::mbar_test(&S.sf_ready[f.st], f.ph);
+                        const int c = MX ? k >> 1 : k;
+                        mma_fp4<MX>(d, da + 2 * k, db + 2 * k, MX && (k & 1) ? idesc2 : idesc0, sfa + 4 * c,
                                     sfb + 4 * c * r_groups, (kt > k0 || k > 0) ? 1u : 0u);
                     }
+                    ptx::mma_commit(&S.sf_free[sb]);
                     ptx::mma_commit(&S.empty[st]);
                 }
-                if (ok) ptx::mma_commit(&S.acc_full);
+                if (ok) ptx::mma_commit(&S.acc_full[acc.st]);
+                acc.next(a.accs);
             }
             // every issued MMA has completed before TMEM is released
             ptx::mma_commit(&S.drain);
             ptx::mbar_wait_drain(&S.drain, 0);
         }
         __syncwarp();
-    } else if (warp < 6) {
-        // ================= scales =================
-        const int r = t - 64;                            // 0..127: a left row and up to two right rows
-        const uint32_t cell = (uint32_t)((r & 31) * 16 + (r >> 5) * 4);
-        int it = 0;
+    } else if (warp < 2 + kLoaders) {
+        // ================= scales to shared memory =================
+        Ring p;
+        int held = 0;
         bool ok = true;
-        for (int64_t tile = first; ok && tile < a.tiles; tile += step) {
-            const TileAt at = tile_at(a, tile);
-            const int64_t rl = at.l0 + r;
-            auto load = [&](int kt, uint4 (&v)[3]) {
-                v[0] = load_scales<MX>(a.left, rl, kt, a.nblk);
-                v[1] = r < NT ? load_scales<MX>(a.right, at.r0 + r, kt, a.nblk) : make_uint4(0u, 0u, 0u, 0u);
-                v[2] = r + 128 < NT ? load_scales<MX>(a.right, at.r0 + 128 + r, kt, a.nblk) : make_uint4(0u, 0u, 0u, 0u);
-            };
-            uint4 cur[3], nxt[3];
-            if (k0 < k1) load(k0, cur);
-            for (int kt = k0; kt < k1; ++kt, ++it) {
-                const int st = it % a.stages;
-                if (kt + 1 < k1) load(kt + 1, nxt);
-                if (it >= a.stages && !ptx::mbar_wait(&S.empty[st], ((it / a.stages) - 1) & 1, abort_flag)) {
-                    ok = false;
-                    break;
+        if (a.sf_tma) {
+            if (warp == 2 && lane == 0) {
+                for (int64_t tile = first; ok && tile < a.tiles; tile += step) {
+                    const TileAt at = tile_at(a, tile);
+                    for (int kt = k0; kt < k1; kt += kChunk) {
+                        if (!ptx::mbar_wait(&S.sf_empty[p.st], p.ph ^ 1, abort_flag)) { ok = false; break; }
+                        uint8_t *ss = sf_mem + p.st * sf_bytes;
+                        // a box of 128 left rows, one of NT right rows
+                        ptx::mbar_arrive_expect_tx(&S.sf_full[p.st], (uint32_t)((kM + NT) * kRow));
+                        ptx::tma_load_2d(ss, &lsmap, kt * 4 * kCells, (int32_t)at.l0, &S.sf_full[p.st]);
+                        ptx::tma_load_2d(ss + kM * kRow, &rsmap, kt * 4 * kCells, (int32_t)at.r0, &S.sf_full[p.st]);
+                        p.next(kChunks);
+                        held = min(held + 1, kChunks);
+                    }
                 }
-                uint8_t *ss = base + (size_t)st * stage_bytes + l_bytes + ((r_bytes + 1023) & ~1023);
-#pragma unroll
-                for (int g = 0; g < 3; ++g) {
-                    if (g > r_groups) break;
-                    const uint32_t w[4] = {cur[g].x, cur[g].y, cur[g].z, cur[g].w};
-#pragma unroll
-                    for (int c = 0; c < kCells; ++c)
-                        *reinterpret_cast<uint32_t *>(ss + 512 * (kCells * g + c) + cell) = w[c];
+                for (; held > 0; --held) {               // the last copies land before the CTA leaves
+                    if (p.st == 0) { p.st = kChunks; p.ph ^= 1; }
+                    --p.st;
+                    ptx::mbar_wait_drain(&S.sf_full[p.st], p.ph);
                 }
-                ptx::fence_async_smem();
-                ptx::mbar_arrive(&S.full[st]);
-#pragma unroll
-                for (int g = 0; g < 3; ++g) cur[g] = nxt[g];
+            }
+        } else {
+            const int lt = t - 64;                       // 0 .. 127
+            constexpr int kPieces = kRow / 16;           // of a row
+            for (int64_t tile = first; ok && tile < a.tiles; tile += step) {
+                const TileAt at = tile_at(a, tile);
+                for (int kt = k0; kt < k1; kt += kChunk) {
+                    ok = ptx::mbar_wait(&S.sf_empty[p.st], p.ph ^ 1, abort_flag);
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    uint8_t *ss = sf_mem + p.st * sf_bytes;
+#pragma unroll 4
+                    for (int i = lt; i < (kM + NT) * kPieces; i += 32 * kLoaders) {
+                        const int row = i / kPieces, q = i % kPieces;
+                        const bool left = row < kM;
+                        const uint4 v = load_scales(left ? a.left : a.right, left ? at.l0 + row : at.r0 + row - kM,
+                                                    kt * 4 * kCells + 16 * q, a.nblk);
+                        *reinterpret_cast<uint4 *>(ss + chunk_off<kCells>(row, q)) = v;
+                    }
+                    ptx::mbar_arrive(&S.sf_full[p.st]);
+                    p.next(kChunks);
+                }
             }
         }
+        __syncwarp();
+    } else if (warp < kEpiWarp0) {
+        // ================= scales to TMEM =================
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        Ring p, f;
+        bool ok = true;
+        for (int64_t tile = first; ok && tile < a.tiles; tile += step)
+            for (int kt = k0, i = 0; kt < k1; ++kt) {
+                ok = ptx::mbar_wait(&S.sf_free[f.st], f.ph ^ 1, abort_flag) &&
+                     (i > 0 || ptx::mbar_wait(&S.sf_full[p.st], p.ph, abort_flag));
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                ptx::tc_fence_after();
+                const uint8_t *ss = sf_mem + p.st * sf_bytes;
+                const uint32_t col = lane_base + sf_col0 + f.st * sf_cols;
+                if (r_groups == 2)
+                    scales_to_tmem<kCells, 2>(ss, i, lane, col);
+                else
+                    scales_to_tmem<kCells, 1>(ss, i, lane, col);
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&S.sf_ready[f.st]);
+                f.next(a.sf_bufs);
+                if (++i == kChunk || kt + 1 == k1) {     // the chunk has been read
+                    if (lane == 0) ptx::mbar_arrive(&S.sf_empty[p.st]);
+                    p.next(kChunks);
+                    i = 0;
+                }
+            }
+        __syncwarp();
     } else {
         // ================= epilogue =================
-        const int half = (warp - 6) >> 2, sub = warp & 3;
-        const uint32_t lane_addr = tmem + ((uint32_t)(sub * 32) << 16);
+        const int half = (warp - kEpiWarp0) >> 2, sub = warp & 3;
+        const uint32_t lane_base = (uint32_t)(sub * 32) << 16;
         const int64_t lrow = sub * 32 + lane;
-        int n = 0;
-        for (int64_t tile = first; tile < a.tiles; tile += step, ++n) {
+        uint8_t *const stg = store0 + (warp - kEpiWarp0) * kStoreBytes;
+        Ring acc;
+        for (int64_t tile = first; tile < a.tiles; tile += step) {
             const TileAt at = tile_at(a, tile);
-            if (!ptx::mbar_wait(&S.acc_full, n & 1, abort_flag)) break;
+            const bool ok = ptx::mbar_wait(&S.acc_full[acc.st], acc.ph, abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) break;
             ptx::tc_fence_after();
+            const uint32_t taddr = tmem + lane_base + acc.st * a.acc_cols;
             if (a.splits > 1) {
                 // this CTA's share of K, column by column: every copy into the stages has been
                 // consumed, so their memory is free
                 float *part = reinterpret_cast<float *>(base);
                 for (int c0 = half * 16; c0 < NT; c0 += 32) {
                     uint32_t u[16];
-                    ptx::tmem_ld16(lane_addr + c0, u);
+                    ptx::tmem_ld16(taddr + c0, u);
                     ptx::tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 16; ++i) part[(c0 + i) * kM + lrow] = __uint_as_float(u[i]);
                 }
-            } else {
-                for (int c0 = half * 32; c0 < NT; c0 += 64) {
-                    float v[32];
-                    {
-                        uint32_t u[32];
-                        if (c0 + 32 <= NT) {
-                            ptx::tmem_ld32(lane_addr + c0, u);
-                        } else {                         // NT is a multiple of 16
-                            uint32_t w[16];
-                            ptx::tmem_ld16(lane_addr + c0, w);
+            } else if (a.out_tma) {
+                // 32 rows x 128 bytes at a time; the halves take alternate pieces
+                constexpr int kCols = BF16 ? 64 : 32;
+                for (int c0 = half * kCols; c0 < NT && at.r0 + c0 < a.right.rows; c0 += 2 * kCols) {
+                    uint32_t w[32];
+                    if (BF16) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) { u[i] = w[i]; u[16 + i] = 0u; }
-                        }
-                        ptx::tmem_ld_wait();
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t u[32];
+                            ptx::tmem_ld32(taddr + c0 + 32 * q, u);
+                            ptx::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]) * a.alpha;
-                    }
-                    // a tile 16 columns wide: the columns past it belong to the next tile
-                    if (c0 + 32 > NT) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int64_t l = at.l0 + lrow, rr = at.r0 + c0 + i;
-                            if (l < a.left.rows && rr < a.right.rows) {
-                                const int64_t o = a.swap ? rr * a.out_stride + l : l * a.out_stride + rr;
-                                if (BF16)
-                                    reinterpret_cast<__nv_bfloat16 *>(a.out)[o] = __float2bfloat16_rn(v[i]);
-                                else
-                                    reinterpret_cast<float *>(a.out)[o] = v[i];
+                            for (int i = 0; i < 16; ++i) {
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(u[2 * i]) * a.alpha,
+                                                                               __uint_as_float(u[2 * i + 1]) * a.alpha);
+                                w[16 * q + i] = *reinterpret_cast<const uint32_t *>(&h);
                             }
                         }
                     } else {
-                        store_cols<BF16>(a, at.l0 + lrow, at.r0 + c0, v);
+                        ptx::tmem_ld32(taddr + c0, w);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * a.alpha);
                     }
+                    if (lane == 0) bulk_wait_read();     // the last store has left the buffer
+                    __syncwarp();
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        *reinterpret_cast<uint4 *>(stg + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                            make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+                    ptx::fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && at.l0 + sub * 32 < a.left.rows) {
+                        tma_store_2d(&omap, stg, (int32_t)(at.r0 + c0), (int32_t)(at.l0 + sub * 32));
+                        ptx::bulk_commit();
+                    }
+                }
+            } else {
+                for (int c0 = half * 32; c0 < NT; c0 += 64) {
+                    const int cols = min(32, NT - c0);   // 32, or 16 at the end: NT is a multiple of 16
+                    uint32_t u[32];
+                    if (cols == 32) {
+                        ptx::tmem_ld32(taddr + c0, u);
+                    } else {
+                        uint32_t h[16];
+                        ptx::tmem_ld16(taddr + c0, h);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) { u[i] = h[i]; u[16 + i] = 0u; }
+                    }
+                    ptx::tmem_ld_wait();
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]) * a.alpha;
+                    store_cols<BF16>(a, at.l0 + lrow, at.r0 + c0, cols, v);
                 }
             }
             ptx::tc_fence_before();
-            ptx::mbar_arrive(&S.acc_empty);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&S.acc_empty[acc.st]);
+            acc.next(a.accs);
         }
+        if (lane == 0) ptx::bulk_wait_all();             // the stores have been made before the CTA leaves
+        __syncwarp();
     }
     if (a.splits > 1) {
         // every CTA of the cluster gets here, whatever happened before: no wait can be left behind
         __syncwarp();
         cluster_sync();
-        if (*abort_flag == 0 && warp >= 6) {
+        if (*abort_flag == 0 && warp >= kEpiWarp0) {
             const TileAt at = tile_at(a, first);
-            const int et = t - 192;
+            const int et = t - 32 * kEpiWarp0;
             const float *part = reinterpret_cast<const float *>(base);
             const int c0 = NT * rank / a.splits, c1 = NT * (rank + 1) / a.splits;
             const int lr = et & (kM - 1);
-            for (int c = c0 + (et >> 7); c < c1; c += kEpiThreads / kM) {
+            for (int c = c0 + (et >> 7); c < c1; c += 32 * kEpiWarps / kM) {
                 float v[kMaxSplits];
 #pragma unroll
                 for (int s = 0; s < kMaxSplits; ++s)
@@ -434,25 +605,25 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
 
 struct Plan {
     bool swap;
-    int NT, splits, stages;
+    int NT, splits, stages, accs, sf_bufs;
 };
 
-inline int stage_bytes_of(bool mx, int NT) {
-    const int cells = mx ? 2 : 4;
-    return kM * 128 + ((NT * 128 + 1023) & ~1023) + ((cells * 512 * (1 + (NT + 127) / 128) + 1023) & ~1023);
-}
+inline int chunk_bytes_of(bool mx, int NT) { return (mx ? 32 : 64) * 128 * (NT > 128 ? 3 : 2); }
+inline int sf_cols_of(bool mx, int NT) { return (mx ? 8 : 16) * (NT > 128 ? 3 : 2); }
+inline int acc_cols_of(int NT) { return NT < 32 ? 32 : NT; }
 
 // Estimated finish time, in SM cycles, of the candidates (operand order, tile width, K splits); the
 // smallest wins.
 inline Plan make_plan(bool mx, int64_t M, int64_t N, int K, int nsm) {
-    Plan best{false, 128, 1, 4};
+    Plan best{false, 128, 1, 4, 2, 2};
     double best_t = 1e300;
     const int ktiles = (K + kKTile - 1) / kKTile;
+    constexpr int widths[5] = {16, 32, 64, 128, 192};
     for (int sw = 0; sw < 2; ++sw)
-        for (int NT = 16; NT <= kMaxNT; NT *= 2)
+        for (int NT : widths)
             for (int sp = 1; sp <= kMaxSplits; sp *= 2) {
                 const int64_t L = sw ? N : M, R = sw ? M : N;
-                if (sp > 1 && (sp > ktiles || NT > 128)) continue;
+                if (sp > 1 && (sp > (mx ? (ktiles + 1) / 2 : ktiles) || NT > 128)) continue;
                 const int64_t tiles = ceil_div(L, kM) * ceil_div(R, NT);
                 const int64_t units = tiles * sp;
                 if (sp > 1 && units > nsm) continue;
@@ -464,16 +635,15 @@ inline Plan make_plan(bool mx, int64_t M, int64_t N, int K, int nsm) {
                 const double t = 2500.0 + waves * (kt * stage + 800.0 + epi) + (sp > 1 ? 1200.0 : 0.0);
                 if (t < best_t) {
                     best_t = t;
-                    best = Plan{sw != 0, NT, sp, 0};
+                    best = Plan{sw != 0, NT, sp, 0, 0, 0};
                 }
             }
-    const int sb = stage_bytes_of(mx, best.NT);
-    int st = (int)((227 * 1024 - 2048 - (int)sizeof(Ctl)) / sb);
-    const int cells = mx ? 2 : 4;
-    const int sf_cols = cells * 4 * (1 + (best.NT + 127) / 128);
-    const int acc = best.NT < 32 ? 32 : best.NT;
-    st = std::min(st, (512 - acc) / sf_cols);
-    best.stages = std::min(st, kMaxStages);
+    const int NT = best.NT;
+    const int stage = kM * 128 + ((NT * 128 + 1023) & ~1023);
+    const int room = 227 * 1024 - 1024 - (int)sizeof(Ctl) - kEpiWarps * kStoreBytes - kChunks * chunk_bytes_of(mx, NT);
+    best.stages = std::min(kMaxStages, room / stage);
+    best.accs = 2;
+    best.sf_bufs = std::min(best.stages, (512 - 2 * acc_cols_of(NT)) / sf_cols_of(mx, NT));
     return best;
 }
 
@@ -482,7 +652,8 @@ inline Plan make_plan(bool mx, int64_t M, int64_t N, int K, int nsm) {
 static SmemLimit g_fmm_smem[4];
 
 template <bool MX, bool BF16>
-static cudaError_t launch_fmm(const fmm::Args &a, const CUtensorMap &lm, const CUtensorMap &rm, int smem, unsigned grid,
+static cudaError_t launch_fmm(const fmm::Args &a, const CUtensorMap &lm, const CUtensorMap &rm, const CUtensorMap &lsm,
+                              const CUtensorMap &rsm, const CUtensorMap &om, int smem, unsigned grid,
                               cudaStream_t st) {
     cudaError_t e = ensure_smem_limit(g_fmm_smem[(MX ? 2 : 0) + (BF16 ? 1 : 0)], fmm::fp4_matmul_kernel<MX, BF16>, smem);
     if (e != cudaSuccess) return e;
@@ -497,7 +668,7 @@ static cudaError_t launch_fmm(const fmm::Args &a, const CUtensorMap &lm, const C
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = a.splits > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, fmm::fp4_matmul_kernel<MX, BF16>, a, lm, rm);
+    e = cudaLaunchKernelEx(&cfg, fmm::fp4_matmul_kernel<MX, BF16>, a, lm, rm, lsm, rsm, om);
     note_launches(1);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
@@ -512,37 +683,51 @@ cudaError_t launch_fp4_matmul(int fmt, const uint8_t *a_codes, int64_t a_code_st
     if (!enc) return cudaErrorNotSupported;
     cudaError_t e = bind_current_context();
     if (e != cudaSuccess) return e;
-    const uintptr_t sf_mask = mx ? 7u : 15u;
     auto operand = [&](const uint8_t *s, int64_t stride, int64_t rows) {
-        return fmm::Operand{s, stride, rows, ((reinterpret_cast<uintptr_t>(s) | (uintptr_t)stride) & sf_mask) == 0};
+        return fmm::Operand{s, stride, rows};
     };
-    auto encode = [&](CUtensorMap *m, const uint8_t *codes, int64_t stride, int64_t rows, int box_rows) {
-        const cuuint64_t dim[2] = {(cuuint64_t)(K / 2), (cuuint64_t)rows};
+    // byte rows: boxes of box_rows rows of `width` bytes, swizzled over that width
+    auto encode = [&](CUtensorMap *m, const uint8_t *base, int64_t bytes, int64_t stride, int64_t rows, int box_rows, int width) {
+        const cuuint64_t dim[2] = {(cuuint64_t)bytes, (cuuint64_t)rows};
         const cuuint64_t strides[1] = {(cuuint64_t)stride};
-        const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+        const cuuint32_t box[2] = {(cuuint32_t)width, (cuuint32_t)box_rows};
         const cuuint32_t ones[2] = {1, 1};
-        return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(codes), dim, strides, box, ones,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+        const CUtensorMapSwizzle sw = width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                   : width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
+        return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(base), dim, strides, box, ones,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
     fmm::Args a;
     CUtensorMap lm, rm;
     a.left = p.swap ? operand(b_scales, b_scale_stride, N) : operand(a_scales, a_scale_stride, M);
     a.right = p.swap ? operand(a_scales, a_scale_stride, M) : operand(b_scales, b_scale_stride, N);
-    const bool ok = p.swap ? encode(&lm, b_codes, b_code_stride, N, fmm::kM) && encode(&rm, a_codes, a_code_stride, M, p.NT)
-                           : encode(&lm, a_codes, a_code_stride, M, fmm::kM) && encode(&rm, b_codes, b_code_stride, N, p.NT);
-    if (!ok) return cudaErrorInvalidValue;
+    const uint8_t *lc = p.swap ? b_codes : a_codes, *rc = p.swap ? a_codes : b_codes;
+    const int64_t lcs = p.swap ? b_code_stride : a_code_stride, rcs = p.swap ? a_code_stride : b_code_stride;
+    if (!encode(&lm, lc, K / 2, lcs, a.left.rows, fmm::kM, 128) || !encode(&rm, rc, K / 2, rcs, a.right.rows, p.NT, 128))
+        return cudaErrorInvalidValue;
+    // scale rows by tensor copies where base and stride allow them
+    CUtensorMap lsm = lm, rsm = rm;
+    const int nblk = K / (mx ? 32 : 16), width = mx ? 32 : 64;
+    auto sf_ok = [](const fmm::Operand &o) {
+        return ((reinterpret_cast<uintptr_t>(o.scales) | (uintptr_t)o.scale_stride) & 15u) == 0 &&
+               o.scale_stride < ((int64_t)1 << 40);
+    };
+    a.sf_tma = sf_ok(a.left) && sf_ok(a.right) &&
+               encode(&lsm, a.left.scales, nblk, a.left.scale_stride, a.left.rows, fmm::kM, width) &&
+               encode(&rsm, a.right.scales, nblk, a.right.scale_stride, a.right.rows, p.NT, width);
     a.K = K;
-    a.nblk = K / (mx ? 32 : 16);
+    a.nblk = nblk;
     a.NT = p.NT;
     a.stages = p.stages;
     a.splits = p.splits;
     a.tiles_l = (int)ceil_div(a.left.rows, (int64_t)fmm::kM);
     a.tiles = (int64_t)a.tiles_l * ceil_div(a.right.rows, (int64_t)p.NT);
     a.ktiles = (K + fmm::kKTile - 1) / fmm::kKTile;
-    const int cells = mx ? 2 : 4;
-    a.acc_cols = (uint32_t)(p.NT < 32 ? 32 : p.NT);
-    const uint32_t need = a.acc_cols + (uint32_t)(p.stages * cells * 4 * (1 + (p.NT + 127) / 128));
+    a.accs = p.accs;
+    a.sf_bufs = p.sf_bufs;
+    a.acc_cols = (uint32_t)fmm::acc_cols_of(p.NT);
+    const uint32_t need = a.accs * a.acc_cols + (uint32_t)(p.sf_bufs * fmm::sf_cols_of(mx, p.NT));
     uint32_t cols = 32;
     while (cols < need) cols <<= 1;
     a.tmem_cols = cols;
@@ -552,13 +737,28 @@ cudaError_t launch_fp4_matmul(int fmt, const uint8_t *a_codes, int64_t a_code_st
     a.out_stride = out_stride;
     const int64_t es = out_dtype == CSA2_DTYPE_BF16 ? 2 : 4;
     a.out_vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && (out_stride * es) % 16 == 0;
-    const int smem = p.stages * fmm::stage_bytes_of(mx, p.NT) + (int)sizeof(fmm::Ctl) + 1024;
+    // whole pieces of 128 bytes along n leave by tensor stores; their rows have to be 16-byte aligned
+    CUtensorMap om = lm;
+    a.out_tma = !p.swap && p.splits == 1 && p.NT % (es == 2 ? 64 : 32) == 0 && a.out_vec;
+    if (a.out_tma) {
+        const cuuint64_t dim[2] = {(cuuint64_t)N, (cuuint64_t)M};
+        const cuuint64_t strides[1] = {(cuuint64_t)(out_stride * es)};
+        const cuuint32_t box[2] = {(cuuint32_t)(128 / es), 32};
+        const cuuint32_t ones[2] = {1, 1};
+        if (out_stride * es >= ((int64_t)1 << 40) ||
+            enc(&om, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, out, dim, strides, box,
+                ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            a.out_tma = false;
+    }
+    const int smem = p.stages * (fmm::kM * 128 + ((p.NT * 128 + 1023) & ~1023)) + fmm::kChunks * fmm::chunk_bytes_of(mx, p.NT) +
+                     (a.out_tma ? fmm::kEpiWarps * fmm::kStoreBytes : 0) + (int)sizeof(fmm::Ctl) + 1024;
     const int64_t grid = p.splits > 1 ? a.tiles * p.splits : std::min<int64_t>(a.tiles, device_sm_count());
     if (mx)
-        return out_dtype == CSA2_DTYPE_BF16 ? launch_fmm<true, true>(a, lm, rm, smem, (unsigned)grid, st)
-                                            : launch_fmm<true, false>(a, lm, rm, smem, (unsigned)grid, st);
-    return out_dtype == CSA2_DTYPE_BF16 ? launch_fmm<false, true>(a, lm, rm, smem, (unsigned)grid, st)
-                                        : launch_fmm<false, false>(a, lm, rm, smem, (unsigned)grid, st);
+        return out_dtype == CSA2_DTYPE_BF16 ? launch_fmm<true, true>(a, lm, rm, lsm, rsm, om, smem, (unsigned)grid, st)
+                                            : launch_fmm<true, false>(a, lm, rm, lsm, rsm, om, smem, (unsigned)grid, st);
+    return out_dtype == CSA2_DTYPE_BF16 ? launch_fmm<false, true>(a, lm, rm, lsm, rsm, om, smem, (unsigned)grid, st)
+                                        : launch_fmm<false, false>(a, lm, rm, lsm, rsm, om, smem, (unsigned)grid, st);
 }
 
 }  // namespace csa2

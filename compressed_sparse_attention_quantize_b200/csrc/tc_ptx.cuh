@@ -34,6 +34,19 @@ CSA2_D bool mbar_try(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
+// One look at a phase, without waiting.
+CSA2_D bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Bounded wait: gives up after 2^22 polls (tenths of a second at least; polls past 2^16 back
 // off with a sleep), records CSA2_ERR_TIMEOUT in the device error word and raises the CTA's
 // abort flag.  The hot waits of the pipelines finish long before the back-off starts: a sleeping
