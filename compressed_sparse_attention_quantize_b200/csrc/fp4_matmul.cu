@@ -74,9 +74,9 @@ struct Args {
 };
 
 struct Ctl {
-    uint64_t full[kMaxStages], empty[kMaxStages];        // the codes are there; the stage is free
+    uint64_t full[kMaxStages];                           // the codes are there, the scales in TMEM
+    uint64_t empty[kMaxStages];                          // the stage's MMAs have completed
     uint64_t sf_full[kChunks], sf_empty[kChunks];        // chunks of scale bytes in shared memory
-    uint64_t sf_ready[kMaxStages], sf_free[kMaxStages];  // TMEM scale buffers
     uint64_t acc_full[2], acc_empty[2], drain;
     uint32_t tmem_base;
     int abort_flag;
@@ -293,16 +293,12 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
 
     if (t == 0) {
         for (int i = 0; i < a.stages; ++i) {
-            ptx::mbar_init(&S.full[i], 1);
+            ptx::mbar_init(&S.full[i], 1 + 4);
             ptx::mbar_init(&S.empty[i], 1);
         }
         for (int i = 0; i < kChunks; ++i) {
             ptx::mbar_init(&S.sf_full[i], a.sf_tma ? 1 : 32 * kLoaders);
             ptx::mbar_init(&S.sf_empty[i], 4);
-        }
-        for (int i = 0; i < a.sf_bufs; ++i) {
-            ptx::mbar_init(&S.sf_ready[i], 4);
-            ptx::mbar_init(&S.sf_free[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&S.acc_full[i], 1);
@@ -364,27 +360,22 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
                 ptx::tc_fence_after();
                 const uint32_t d = tmem + acc.st * a.acc_cols;
                 for (int kt = k0; kt < k1; ++kt) {
-                    if (!seen && (!ptx::mbar_wait(&S.full[p.st], p.ph, abort_flag) ||
-                                  !ptx::mbar_wait(&S.sf_ready[f.st], f.ph, abort_flag))) {
-                        ok = false;
-                        break;
-                    }
+                    if (!seen && !ptx::mbar_wait(&S.full[p.st], p.ph, abort_flag)) { ok = false; break; }
                     ptx::tc_fence_after();
                     const uint32_t sfa = sf_col0 + f.st * sf_cols, sfb = sfa + kCells * 4;
                     const uint64_t da = da0 + p.st * stage16, db = da + l16;
-                    const int st = p.st, sb = f.st;
+                    const int st = p.st;
                     p.next(a.stages);
                     f.next(a.sf_bufs);
 #pragma unroll
                     for (int k = 0; k < kSteps; ++k) {
-                        // the next stage's barriers are polled while the tensor pipe still has work
-                        if (k == kSteps - 1)
-                            seen = ptx::mbar_test(&S.full[p.st], p.ph) && ptx::mbar_test(&S.sf_ready[f.st], f.ph);
+                        // the next stage's barrier is polled while the tensor pipe still has work: a wait
+                        // takes about 150 cycles even when it is over, a stage's MMAs 2 NT
+                        if (k == kSteps - 1) seen = ptx::mbar_test(&S.full[p.st], p.ph);
                         const int c = MX ? k >> 1 : k;
                         mma_fp4<MX>(d, da + 2 * k, db + 2 * k, MX && (k & 1) ? idesc2 : idesc0, sfa + 4 * c,
                                     sfb + 4 * c * r_groups, (kt > k0 || k > 0) ? 1u : 0u);
                     }
-                    ptx::mma_commit(&S.sf_free[sb]);
                     ptx::mma_commit(&S.empty[st]);
                 }
                 if (ok) ptx::mma_commit(&S.acc_full[acc.st]);
@@ -447,11 +438,15 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
     } else if (warp < kEpiWarp0) {
         // ================= scales to TMEM =================
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        Ring p, f;
+        // p: chunks, f: TMEM buffers, u: stages, back: the stage whose MMAs last read buffer f, which
+        // is sf_bufs stages behind u
+        Ring p, f, u, back;
+        back.ph = 1;
+        for (int i = 0; i < a.stages - a.sf_bufs; ++i) back.next(a.stages);
         bool ok = true;
         for (int64_t tile = first; ok && tile < a.tiles; tile += step)
             for (int kt = k0, i = 0; kt < k1; ++kt) {
-                ok = ptx::mbar_wait(&S.sf_free[f.st], f.ph ^ 1, abort_flag) &&
+                ok = ptx::mbar_wait(&S.empty[back.st], back.ph, abort_flag) &&
                      (i > 0 || ptx::mbar_wait(&S.sf_full[p.st], p.ph, abort_flag));
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 ptx::tc_fence_after();
@@ -464,8 +459,10 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&S.sf_ready[f.st]);
+                if (lane == 0) ptx::mbar_arrive(&S.full[u.st]);
                 f.next(a.sf_bufs);
+                u.next(a.stages);
+                back.next(a.stages);
                 if (++i == kChunk || kt + 1 == k1) {     // the chunk has been read
                     if (lane == 0) ptx::mbar_arrive(&S.sf_empty[p.st]);
                     p.next(kChunks);
