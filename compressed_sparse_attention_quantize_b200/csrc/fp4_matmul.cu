@@ -9,8 +9,8 @@
 // columns, instead of padding the batch to 128 rows.  Per 256 channels (a stage):
 //   warp 0        the codes of both operands by tensor copies (128-byte rows, 128-byte swizzle; rows
 //                 and channels past the end arrive as zeros)
-//   warp 2        the scale bytes of four stages at a time (64 or 32 a row) by tensor copies, two such
-//                 chunks in flight.  16 bytes a row and stage through the load units held the whole
+//   warp 2        the scale bytes of four stages at a time (64 or 32 a row) by tensor copies, two to
+//                 four such chunks in flight.  16 bytes a row and stage through the load units held the whole
 //                 kernel up, each in a cache line of its own (137 us at 4096 x 8192 x 4096).  Rows that
 //                 are not 16-byte aligned come through registers (warps 2-5).  Scales past the end are
 //                 zero: a NaN there would survive the zero codes.
@@ -42,7 +42,7 @@ constexpr int kMaxNT = 192;
 constexpr int kThreads = 576;
 constexpr int kLoaders = 4;                // scale-loading warps
 constexpr int kChunk = 4;                  // stages of scales loaded at a time
-constexpr int kChunks = 2;                 // such chunks in shared memory
+constexpr int kMaxChunks = 4;              // such chunks in shared memory
 constexpr int kEpiWarps = 8;
 constexpr int kEpiWarp0 = 10;
 constexpr int kMaxStages = 8;
@@ -60,6 +60,7 @@ struct Args {
     int K, nblk;                           // channels, scale blocks per row
     int NT, stages, splits;
     int accs, sf_bufs;                     // accumulators, stages of scales in TMEM
+    int chunks;                            // chunks of scales in shared memory
     int tiles_l;                           // left tiles
     int64_t tiles;                         // all tiles
     int ktiles;                            // stages of the whole K
@@ -76,7 +77,7 @@ struct Args {
 struct Ctl {
     uint64_t full[kMaxStages];                           // the codes are there, the scales in TMEM
     uint64_t empty[kMaxStages];                          // the stage's MMAs have completed
-    uint64_t sf_full[kChunks], sf_empty[kChunks];        // chunks of scale bytes in shared memory
+    uint64_t sf_full[kMaxChunks], sf_empty[kMaxChunks];        // chunks of scale bytes in shared memory
     uint64_t acc_full[2], acc_empty[2], drain;
     uint32_t tmem_base;
     int abort_flag;
@@ -157,11 +158,12 @@ CSA2_D void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-CSA2_D float ld_peer(const float *p, uint32_t rank) {
+CSA2_D float4 ld_peer4(const float *p, uint32_t rank) {
     uint32_t a;
-    float v;
+    float4 v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
     return v;
 }
 
@@ -281,7 +283,7 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
     // the stages' codes, the epilogue warps' output tiles, the chunks of scales, the barriers
     uint8_t *const store0 = base + (size_t)a.stages * code_bytes;
     uint8_t *const sf_mem = store0 + (a.out_tma ? kEpiWarps * kStoreBytes : 0);
-    Ctl &S = *reinterpret_cast<Ctl *>(sf_mem + kChunks * sf_bytes);
+    Ctl &S = *reinterpret_cast<Ctl *>(sf_mem + a.chunks * sf_bytes);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
 
     const int rank = a.splits > 1 ? (int)(blockIdx.x % a.splits) : 0;
@@ -296,7 +298,7 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
             ptx::mbar_init(&S.full[i], 1 + 4);
             ptx::mbar_init(&S.empty[i], 1);
         }
-        for (int i = 0; i < kChunks; ++i) {
+        for (int i = 0; i < a.chunks; ++i) {
             ptx::mbar_init(&S.sf_full[i], a.sf_tma ? 1 : 32 * kLoaders);
             ptx::mbar_init(&S.sf_empty[i], 4);
         }
@@ -402,12 +404,12 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
                         ptx::mbar_arrive_expect_tx(&S.sf_full[p.st], (uint32_t)((kM + NT) * kRow));
                         ptx::tma_load_2d(ss, &lsmap, kt * 4 * kCells, (int32_t)at.l0, &S.sf_full[p.st]);
                         ptx::tma_load_2d(ss + kM * kRow, &rsmap, kt * 4 * kCells, (int32_t)at.r0, &S.sf_full[p.st]);
-                        p.next(kChunks);
-                        held = min(held + 1, kChunks);
+                        p.next(a.chunks);
+                        held = min(held + 1, a.chunks);
                     }
                 }
                 for (; held > 0; --held) {               // the last copies land before the CTA leaves
-                    if (p.st == 0) { p.st = kChunks; p.ph ^= 1; }
+                    if (p.st == 0) { p.st = a.chunks; p.ph ^= 1; }
                     --p.st;
                     ptx::mbar_wait_drain(&S.sf_full[p.st], p.ph);
                 }
@@ -430,7 +432,7 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
                         *reinterpret_cast<uint4 *>(ss + chunk_off<kCells>(row, q)) = v;
                     }
                     ptx::mbar_arrive(&S.sf_full[p.st]);
-                    p.next(kChunks);
+                    p.next(a.chunks);
                 }
             }
         }
@@ -465,7 +467,7 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
                 back.next(a.stages);
                 if (++i == kChunk || kt + 1 == k1) {     // the chunk has been read
                     if (lane == 0) ptx::mbar_arrive(&S.sf_empty[p.st]);
-                    p.next(kChunks);
+                    p.next(a.chunks);
                     i = 0;
                 }
             }
@@ -568,24 +570,31 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
             const int et = t - 32 * kEpiWarp0;
             const float *part = reinterpret_cast<const float *>(base);
             const int c0 = NT * rank / a.splits, c1 = NT * (rank + 1) / a.splits;
-            const int lr = et & (kM - 1);
-            for (int c = c0 + (et >> 7); c < c1; c += 32 * kEpiWarps / kM) {
-                float v[kMaxSplits];
+            // four lanes of one column per thread: the cluster's shared memory is read in 16-byte pieces
+            const int lr = (et & 31) * 4;
+            for (int c = c0 + (et >> 5); c < c1; c += kEpiWarps) {
+                float4 v[kMaxSplits];
 #pragma unroll
                 for (int s = 0; s < kMaxSplits; ++s)
-                    if (s < a.splits) v[s] = ld_peer(part + c * kM + lr, s);
-                float sum = 0.0f;
+                    if (s < a.splits) v[s] = ld_peer4(part + c * kM + lr, s);
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int s = 0; s < kMaxSplits; ++s)
-                    if (s < a.splits) sum += v[s];
-                sum *= a.alpha;
-                const int64_t l = at.l0 + lr, rr = at.r0 + c;
-                if (l < a.left.rows && rr < a.right.rows) {
-                    const int64_t o = a.swap ? rr * a.out_stride + l : l * a.out_stride + rr;
-                    if (BF16)
-                        reinterpret_cast<__nv_bfloat16 *>(a.out)[o] = __float2bfloat16_rn(sum);
-                    else
-                        reinterpret_cast<float *>(a.out)[o] = sum;
+                    if (s < a.splits) {
+                        sum[0] += v[s].x; sum[1] += v[s].y; sum[2] += v[s].z; sum[3] += v[s].w;
+                    }
+                const int64_t rr = at.r0 + c;
+                if (rr < a.right.rows) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int64_t l = at.l0 + lr + k;
+                        if (l >= a.left.rows) break;
+                        const int64_t o = rr * a.out_stride + l;         // K is split with tokens as columns only
+                        if (BF16)
+                            reinterpret_cast<__nv_bfloat16 *>(a.out)[o] = __float2bfloat16_rn(sum[k] * a.alpha);
+                        else
+                            reinterpret_cast<float *>(a.out)[o] = sum[k] * a.alpha;
+                    }
                 }
             }
         }
@@ -602,7 +611,7 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
 
 struct Plan {
     bool swap;
-    int NT, splits, stages, accs, sf_bufs;
+    int NT, splits, stages, accs, sf_bufs, chunks;
 };
 
 inline int chunk_bytes_of(bool mx, int NT) { return (mx ? 32 : 64) * 128 * (NT > 128 ? 3 : 2); }
@@ -612,7 +621,7 @@ inline int acc_cols_of(int NT) { return NT < 32 ? 32 : NT; }
 // Estimated finish time, in SM cycles, of the candidates (operand order, tile width, K splits); the
 // smallest wins.
 inline Plan make_plan(bool mx, int64_t M, int64_t N, int K, int nsm) {
-    Plan best{false, 128, 1, 4, 2, 2};
+    Plan best{false, 128, 1, 4, 2, 2, 2};
     double best_t = 1e300;
     const int ktiles = (K + kKTile - 1) / kKTile;
     constexpr int widths[5] = {16, 32, 64, 128, 192};
@@ -620,25 +629,30 @@ inline Plan make_plan(bool mx, int64_t M, int64_t N, int K, int nsm) {
         for (int NT : widths)
             for (int sp = 1; sp <= kMaxSplits; sp *= 2) {
                 const int64_t L = sw ? N : M, R = sw ? M : N;
-                if (sp > 1 && (sp > (mx ? (ktiles + 1) / 2 : ktiles) || NT > 128)) continue;
+                // K is split with tokens as columns only: the shares are then stored along the lanes
+                if (sp > 1 && (!sw || sp > (mx ? (ktiles + 1) / 2 : ktiles) || NT > 128)) continue;
                 const int64_t tiles = ceil_div(L, kM) * ceil_div(R, NT);
                 const int64_t units = tiles * sp;
                 if (sp > 1 && units > nsm) continue;
                 const double kt = (double)ktiles / sp;
-                // a stage: the MMAs (128 x NT x 64 in NT / 2 cycles), or its bytes through shared memory
-                const double stage = std::max(2.0 * NT, (kM + NT) * 144.0 / 48.0);
+                // a stage: its MMAs (128 x NT x 64 in NT / 2 cycles) and about 250 cycles around them, or
+                // its bytes through shared memory
+                const double stage = std::max(2.0 * NT + 250.0, (kM + NT) * 144.0 / 48.0);
                 const double waves = (double)ceil_div(units, (int64_t)nsm);
-                const double epi = sw ? 6.0 * NT : 4.0 * NT;
-                const double t = 2500.0 + waves * (kt * stage + 800.0 + epi) + (sp > 1 ? 1200.0 : 0.0);
+                const double epi = sw ? 8.0 * NT : 4.0 * NT;
+                // the cluster's sum reads the other CTAs' shared memory at about 12 bytes a cycle
+                const double join = sp > 1 ? 1500.0 + 512.0 * NT * (sp - 1) / sp / 12.0 : 0.0;
+                const double t = 2500.0 + waves * (kt * stage + 800.0 + epi) + join;
                 if (t < best_t) {
                     best_t = t;
-                    best = Plan{sw != 0, NT, sp, 0, 0, 0};
+                    best = Plan{sw != 0, NT, sp, 0, 0, 0, 0};
                 }
             }
     const int NT = best.NT;
     const int stage = kM * 128 + ((NT * 128 + 1023) & ~1023);
-    const int room = 227 * 1024 - 1024 - (int)sizeof(Ctl) - kEpiWarps * kStoreBytes - kChunks * chunk_bytes_of(mx, NT);
-    best.stages = std::min(kMaxStages, room / stage);
+    const int room = 227 * 1024 - 1024 - (int)sizeof(Ctl) - kEpiWarps * kStoreBytes;
+    best.chunks = NT <= 64 ? kMaxChunks : 2;
+    best.stages = std::min(kMaxStages, (room - best.chunks * chunk_bytes_of(mx, NT)) / stage);
     best.accs = 2;
     best.sf_bufs = std::min(best.stages, (512 - 2 * acc_cols_of(NT)) / sf_cols_of(mx, NT));
     return best;
@@ -723,6 +737,7 @@ cudaError_t launch_fp4_matmul(int fmt, const uint8_t *a_codes, int64_t a_code_st
     a.ktiles = (K + fmm::kKTile - 1) / fmm::kKTile;
     a.accs = p.accs;
     a.sf_bufs = p.sf_bufs;
+    a.chunks = p.chunks;
     a.acc_cols = (uint32_t)fmm::acc_cols_of(p.NT);
     const uint32_t need = a.accs * a.acc_cols + (uint32_t)(p.sf_bufs * fmm::sf_cols_of(mx, p.NT));
     uint32_t cols = 32;
@@ -748,7 +763,7 @@ cudaError_t launch_fp4_matmul(int fmt, const uint8_t *a_codes, int64_t a_code_st
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             a.out_tma = false;
     }
-    const int smem = p.stages * (fmm::kM * 128 + ((p.NT * 128 + 1023) & ~1023)) + fmm::kChunks * fmm::chunk_bytes_of(mx, p.NT) +
+    const int smem = p.stages * (fmm::kM * 128 + ((p.NT * 128 + 1023) & ~1023)) + p.chunks * fmm::chunk_bytes_of(mx, p.NT) +
                      (a.out_tma ? fmm::kEpiWarps * fmm::kStoreBytes : 0) + (int)sizeof(fmm::Ctl) + 1024;
     const int64_t grid = p.splits > 1 ? a.tiles * p.splits : std::min<int64_t>(a.tiles, device_sm_count());
     if (mx)
