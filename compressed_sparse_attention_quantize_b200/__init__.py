@@ -19,7 +19,7 @@ __all__ = [
     "csa2_quantize_kv", "csa2_quantize_kv_batch", "quant_job", "QuantJob", "csa2_compress_quantize_kv", "csa2_index_topk", "csa2_index_topk_workspace_size",
     "csa2_index_topk_scored", "csa2_topk_merge_shards", "csa2_topk_merge_shards_workspace_size",
     "csa2_attn_merge_shards", "csa2_sparse_attn_shard", "csa2_pool_extend", "csa2_page_maps", "csa2_page_ids",
-    "csa2_fp4_matmul", "csa2_fp4_matmul_workspace_size",
+    "csa2_fp4_matmul", "csa2_fp4_matmul_workspace_size", "csa2_prefix_attn", "csa2_prefix_attn_workspace_size",
     "csa2_sparse_attn", "csa2_sparse_attn_workspace_size", "csa2_sparse_attn_plan", "csa2_sparse_attn_noalloc",
     "csa2_layer_group", "csa2_layer_group_workspace_size", "csa2_device_error", "csa2_selftest_bounded_wait",
     "csa2_status_string", "csa2_version", "csa2_launch_count", "GroupDesc", "LayerDesc",
@@ -149,6 +149,11 @@ def lib():
     L.csa2_fp4_matmul.restype = _i32
     L.csa2_fp4_matmul.argtypes = [_i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i32, _f32, _vp,
                                   _i32, _i64, _vp, _sz, _vp]
+    L.csa2_prefix_attn_workspace_size.restype = _i32
+    L.csa2_prefix_attn_workspace_size.argtypes = [_i32, _i32, _i32, _i64, ctypes.POINTER(_sz)]
+    L.csa2_prefix_attn.restype = _i32
+    L.csa2_prefix_attn.argtypes = [_vp, _i32, _i32, _i32, _vp, _i32, _vp, _i64, _i64, _vp, _vp, _i32, _i32, _vp, _i64,
+                                   _f32, _vp, _vp, _vp, _i32, _vp, _vp, _sz, _vp]
     L.csa2_page_maps.restype = _i32
     L.csa2_page_maps.argtypes = [_vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp,
                                  _vp, _i64, _vp, _vp, _vp, _i64, _vp]
@@ -356,6 +361,22 @@ def csa2_fp4_matmul(fmt, a_codes, a_code_stride, a_scales, a_scale_stride, b_cod
     _check(lib().csa2_fp4_matmul(fmt, _ptr(a_codes), a_code_stride, _ptr(a_scales), a_scale_stride, _ptr(b_codes),
                                  b_code_stride, _ptr(b_scales), b_scale_stride, M, N, K, alpha, _ptr(out), out_dtype,
                                  out_stride, _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def csa2_prefix_attn_workspace_size(rows, H, G, max_n) -> int:
+    out = _sz(0)
+    _check(lib().csa2_prefix_attn_workspace_size(rows, H, G, max_n, ctypes.byref(out)))
+    return out.value
+
+
+def csa2_prefix_attn(q, rows, H, D, row_start, G, kv, kv_row_stride, kv_rows, seq_start, table, max_pages,
+                     page_entries, n_prefix, max_n, softmax_scale, own_out, own_lse, out, out_dtype, lse,
+                     workspace, ws_bytes, stream=None) -> None:
+    """Attention over a prefix the rows of a group share, merged with each row's own part (see include/csa2.h)."""
+    _check(lib().csa2_prefix_attn(_ptr(q), rows, H, D, _ptr(row_start), G, _ptr(kv), kv_row_stride, kv_rows,
+                                  _ptr(seq_start), _ptr(table), max_pages, page_entries, _ptr(n_prefix), max_n,
+                                  softmax_scale, _ptr(own_out), _ptr(own_lse), _ptr(out), out_dtype, _ptr(lse),
+                                  _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 def csa2_page_maps(old_tokens, new_tokens, B, ratio, page_entries, window, table, max_pages, free_pages, n_free,

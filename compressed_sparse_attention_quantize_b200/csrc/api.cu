@@ -23,6 +23,10 @@ cudaError_t launch_quant_fp4(int, const void *, int, int64_t, int, int64_t, uint
 cudaError_t launch_quant_fp8_token(const void *, int, int64_t, int, int64_t, uint8_t *, int64_t,
                                    uint8_t *, int64_t, const int64_t *, cudaStream_t);
 cudaError_t launch_quant_batch(const csa2_quant_job *, int, cudaStream_t);
+size_t prefix_attn_workspace_bytes(int, int, int, int64_t);
+cudaError_t launch_prefix_attn(const uint16_t *, int, int, const int32_t *, int, const uint8_t *, int64_t, int64_t,
+                               const int64_t *, const int32_t *, int, int, const int32_t *, int64_t, float,
+                               const float *, const float *, void *, int, float *, void *, cudaStream_t);
 cudaError_t launch_fp4_matmul(int, const uint8_t *, int64_t, const uint8_t *, int64_t, const uint8_t *, int64_t,
                               const uint8_t *, int64_t, int64_t, int64_t, int, float, void *, int, int64_t,
                               cudaStream_t);
@@ -385,6 +389,45 @@ csa2_status csa2_page_ids(const int32_t *ids, int B, int T, int K, const int32_t
         return CSA2_ERR_SHAPE;
     if (!aligned_to(ids, 4) || !aligned_to(table, 4) || !aligned_to(out, 4)) return CSA2_ERR_ALIGN;
     return cuda_status(launch_page_ids(ids, (int64_t)B * T, T, K, table, max_pages, page_entries, out, as_stream(stream)));
+}
+
+static csa2_status check_prefix_shape(int rows, int H, int G, int64_t max_n) {
+    if (H < 16 || H > CSA2_MAX_HEADS || (H % 16)) return CSA2_ERR_SHAPE;
+    if (rows < 1 || (int64_t)rows * H > (1 << 24)) return CSA2_ERR_SHAPE;
+    if (G < 1 || G > CSA2_MAX_PREFIX_GROUPS || max_n < 0 || max_n > (1 << 26) || G * max_n > (1 << 30)) return CSA2_ERR_SHAPE;
+    return CSA2_OK;
+}
+
+csa2_status csa2_prefix_attn_workspace_size(int rows, int H, int G, int64_t max_n, size_t *bytes) {
+    if (!bytes) return CSA2_ERR_INVALID_ARG;
+    const csa2_status s = check_prefix_shape(rows, H, G, max_n);
+    if (s != CSA2_OK) return s;
+    *bytes = round_up(prefix_attn_workspace_bytes(rows, H, G, max_n));
+    return CSA2_OK;
+}
+
+csa2_status csa2_prefix_attn(const uint16_t *q, int rows, int H, int D, const int32_t *row_start, int G, const uint8_t *kv,
+                             int64_t kv_row_stride, int64_t kv_rows, const int64_t *seq_start, const int32_t *table,
+                             int max_pages, int page_entries, const int32_t *n_prefix, int64_t max_n,
+                             float softmax_scale, const float *own_out, const float *own_lse, void *out, int out_dtype,
+                             float *lse, void *workspace, size_t ws_bytes, void *stream) {
+    const Range range("csa2_prefix_attn");
+    if (!q || !row_start || !kv || !n_prefix || !out || (!table && !seq_start) || (!own_out != !own_lse))
+        return CSA2_ERR_INVALID_ARG;
+    if (out_dtype != CSA2_DTYPE_F32 && out_dtype != CSA2_DTYPE_BF16) return CSA2_ERR_INVALID_ARG;
+    if (D != CSA2_LATENT_DIM) return CSA2_ERR_UNSUPPORTED;
+    const csa2_status s = check_prefix_shape(rows, H, G, max_n);
+    if (s != CSA2_OK) return s;
+    if (kv_rows < 0 || kv_row_stride < kKvRowBytes) return CSA2_ERR_SHAPE;
+    if (table && (max_pages < 1 || page_entries < 1 || page_entries > (1 << 20))) return CSA2_ERR_SHAPE;
+    if (!aligned16(q) || !aligned16(kv) || (kv_row_stride & 15) || !aligned16(own_out) || !aligned16(out) ||
+        !aligned_to(row_start, 4) || !aligned_to(seq_start, 8) || !aligned_to(table, 4) || !aligned_to(n_prefix, 4) ||
+        !aligned_to(own_lse, 4) || !aligned_to(lse, 4))
+        return CSA2_ERR_ALIGN;
+    if (!workspace || ws_bytes < round_up(prefix_attn_workspace_bytes(rows, H, G, max_n))) return CSA2_ERR_WORKSPACE;
+    return cuda_status(launch_prefix_attn(q, rows, H, row_start, G, kv, kv_row_stride, kv_rows, seq_start, table, max_pages,
+                                          page_entries, n_prefix, max_n, softmax_scale, own_out, own_lse, out, out_dtype,
+                                          lse, workspace, as_stream(stream)));
 }
 
 csa2_status csa2_attn_merge_shards(const float *outs, const float *lses, int G, int rows, int H, int D,

@@ -568,6 +568,54 @@ CSA2_API csa2_status csa2_page_ids(const int32_t *ids, int B, int T, int K, cons
                                    int page_entries, int32_t *out, void *stream);
 
 /* ------------------------------------------------------------------------------------
+ * csa2_prefix_attn -- attention of a batch over a prefix that its requests share, computed once
+ * for all of them, merged with each row's own part.
+ *
+ * Rows r = 0 .. rows-1 come in G groups: group g's rows are row_start[g] .. row_start[g+1] - 1
+ * and every one of them attends to all n_prefix[g] entries of the group's prefix (main-KV rows as in
+ * csa2_sparse_attn: keys = values = the dequantised 512-wide latent, [B] sections
+ * "CSA2：三层压缩一次吃满" and "FP4 量化 + Bounded Replay").  For row r and head h:
+ *     z_j = softmax_scale * (q[r,h] . v_j), j < n;  own part: z_own = own_lse[r,h], v_own = own_out[r,h]
+ *     out[r,h] = sum_x softmax(z)_x v_x,  lse[r,h] = log(sum_x exp(z_x))  over x = the entries and own
+ * The own part is the fp32 output and natural-log LSE of an attention over the row's own keys
+ * (csa2_sparse_attn with the request's selection and window); own_lse = -inf means none, and both
+ * pointers may be NULL.  A row outside every group, or of a group without entries, gets its own
+ * part; out = 0 and lse = -inf where that is empty too.
+ *
+ * Layouts: q bf16 [rows][H][D]; row_start int32 [G+1] ascending; n_prefix int32 [G] with
+ *   0 <= n_prefix[g] <= max_n (host bound); entry j of group g is cache row
+ *   table[g][j / page_entries] * page_entries + j % page_entries (table int32 [G][max_pages]) or, with
+ *   table NULL, seq_start[g] + j; it holds 288 bytes at kv + row*kv_row_stride; kv has kv_rows rows.
+ *   own_out f32 [rows][H][D], own_lse f32 [rows][H] (both or neither); out [rows][H][D] of out_dtype
+ *   (may be own_out when fp32); lse f32 [rows][H] or NULL (may be own_lse).
+ *   An entry on a page that is not there (-1, or beyond max_pages) or on a row outside [0, kv_rows)
+ *   is left out and the device error word becomes CSA2_ERR_INVALID_ARG; a group whose rows or
+ *   length break the contract is taken as having no rows and the word becomes CSA2_ERR_SHAPE.
+ * Numerics: logits and sums in fp32, weights rounded to fp16 (11 bits, at least 2^-32 of the largest)
+ *   for the product with the exact fp16 entries.
+ * Limits: D == 512; H a multiple of 16, 16 <= H <= CSA2_MAX_HEADS; 1 <= G <= CSA2_MAX_PREFIX_GROUPS;
+ *   q, kv, kv_row_stride, own_out and out 16-byte aligned.
+ * Workspace: csa2_prefix_attn_workspace_size(rows, H, G, max_n, &bytes): the prefixes in fp16 (1 KB
+ *   per entry of G * max_n), the queries (1 KB per head), partials (128 KB per 64 queries and SM).
+ *   Calls that may overlap (other streams, two graphs) need workspaces of their own.
+ * Errors: INVALID_ARG (NULL q, row_start, kv, n_prefix, out, or both table and seq_start; one of own_out
+ *   and own_lse without the other; unknown out_dtype), SHAPE (rows < 1 or rows * H > 2^24, H, G, max_n < 0
+ *   or > 2^26, G * max_n > 2^30, kv_rows < 0, kv_row_stride < 288, page_entries < 1 or > 2^20 or max_pages < 1
+ *   with a table), ALIGN (also an int64 array not 8-byte or an int32 or lse array not 4-byte
+ *   aligned), UNSUPPORTED (D != 512), WORKSPACE, CUDA.
+ * ---------------------------------------------------------------------------------- */
+#define CSA2_MAX_PREFIX_GROUPS 1024
+
+CSA2_API csa2_status csa2_prefix_attn_workspace_size(int rows, int H, int G, int64_t max_n, size_t *bytes);
+CSA2_API csa2_status csa2_prefix_attn(const uint16_t *q, int rows, int H, int D, const int32_t *row_start, int G,
+                                      const uint8_t *kv, int64_t kv_row_stride, int64_t kv_rows,
+                                      const int64_t *seq_start, const int32_t *table, int max_pages,
+                                      int page_entries, const int32_t *n_prefix, int64_t max_n,
+                                      float softmax_scale, const float *own_out, const float *own_lse,
+                                      void *out, int out_dtype, float *lse, void *workspace, size_t ws_bytes,
+                                      void *stream);
+
+/* ------------------------------------------------------------------------------------
  * csa2_device_error -- reads (and clears) the library's device-side error word for the
  * current device: 0 when nothing was recorded since the last call, otherwise the first
  * csa2_status code a kernel recorded: CSA2_ERR_TIMEOUT (a bounded wait expired),
