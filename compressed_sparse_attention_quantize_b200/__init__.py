@@ -199,12 +199,29 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+_current_raw_stream = None
+
+
+def _find_current_raw_stream():
+    """A function giving the current stream's address of the current device.  PyTorch's own raw
+    lookup takes 0.2 us where ``is_available`` and the stream object take 4.3 us, as long as a call
+    itself; the object is used where that lookup is missing."""
+    import torch
+    if not torch.cuda.is_available():
+        raise CSA2Error("no CUDA device")
+    torch.cuda.current_stream()                          # initialises CUDA
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(device())
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        if not torch.cuda.is_available():
-            raise CSA2Error("no CUDA device")
-        return torch.cuda.current_stream().cuda_stream
+        global _current_raw_stream
+        if _current_raw_stream is None:
+            _current_raw_stream = _find_current_raw_stream()
+        return _current_raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
