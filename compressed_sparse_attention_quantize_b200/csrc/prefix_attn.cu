@@ -21,8 +21,9 @@
 //
 // Tile arithmetic, as in csa2_sparse_attn's kernel, with the entries already fp16:
 //   S^T[key, query] = V . Q^T     M=128 keys, N=64 queries, K=512: A = V (K-major), B = Q (K-major)
-//   softmax                       one key per thread, 32 queries; running maxima that move only when
-//                                 some logit exceeds them by 2^8; sums of the unrounded fp32 weights
+//   softmax                       16 warps: one key per thread, 16 queries; running maxima that move
+//                                 only when some logit exceeds them by 2^8; sums of the unrounded fp32
+//                                 weights, per key in registers until the end
 //   O^T[chan, query] += V^T.P^T   four blocks of M=128 channels, N=64, K=128 keys: the same V bytes
 // P is rounded to fp16 with the weights scaled to at most 2^15 (the maximum itself to 2^7), so weights
 // down to 2^-21 of the maximum keep 11 bits and the rest an absolute 2^-32: the rounding is at most
@@ -47,12 +48,14 @@ constexpr int kVRegion = kTile * 128;      // 16 KB
 constexpr int kQBytes = 8 * kQRegion;
 constexpr int kVBytes = 8 * kVRegion;
 constexpr int kPBytes = kTile * kQ * 2;
-constexpr int kThreads = 320;              // copies, MMA issuer, 8 workers
-constexpr int kWorkers = 256;
+constexpr int kThreads = 576;              // copies, MMA issuer, 16 softmax warps
+constexpr int kWorkerWarps = 16;
+constexpr int kCols = 16;                  // queries per softmax warp
 constexpr int kTmemCols = 512;
 constexpr int kOCol = 128;                 // O^T accumulators; S^T at column 0
 constexpr float kShift = 7.0f;             // log2 of the weight of the running maximum
 constexpr float kLag = 8.0f;               // log2 units a logit may exceed the running maximum by
+constexpr float kOver = 32768.0f;          // a weight above 2^(kShift + kLag): the maximum moves
 constexpr int kPartFloats = 2 * kQ + kQ * kLatent;
 
 // Per group, in the workspace (written by the first launch): first query row, first query tile and
@@ -254,6 +257,28 @@ struct Ctl {
 };
 constexpr int kSmemBytes = kQBytes + kVBytes + kPBytes + (int)sizeof(Ctl) + 1024;
 
+// Reduce 16 values over a warp's lanes: afterwards v[0] of lanes c and c + 16 holds the maximum (or sum)
+// of element c.
+template <bool kSum>
+CSA2_D void reduce16(float (&v)[kCols], int lane) {
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+        const float o = __shfl_xor_sync(0xffffffffu, v[i], 16);
+        v[i] = kSum ? v[i] + o : fmaxf(v[i], o);
+    }
+#pragma unroll
+    for (int off = 8, n = 8; off >= 1; off >>= 1, n >>= 1) {
+        const bool upper = (lane & off) != 0;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float send = upper ? v[i] : v[i + n];
+            const float keep = upper ? v[i + n] : v[i];
+            const float got = __shfl_xor_sync(0xffffffffu, send, off);
+            v[i] = kSum ? keep + got : fmaxf(keep, got);
+        }
+    }
+}
+
 // A run of key tiles of one query tile: what a CTA does between two changes of Q.
 struct Segment {
     int64_t tile;                          // query tile
@@ -303,9 +328,9 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap vmap, const
         }
         ptx::mbar_init(&S.q_full, 1);
         ptx::mbar_init(&S.s_full, 1);
-        ptx::mbar_init(&S.p_full, kWorkers / 32);
+        ptx::mbar_init(&S.p_full, kWorkerWarps);
         ptx::mbar_init(&S.seg_done, 1);
-        ptx::mbar_init(&S.o_free, kWorkers / 32);
+        ptx::mbar_init(&S.o_free, kWorkerWarps);
         ptx::mbar_init(&S.drain, 1);
         S.abort_flag = 0;
         ptx::fence_async_smem();
@@ -369,7 +394,7 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap vmap, const
             const uint64_t pv_a0 = ptx::sdesc_sw128(ptx::smem_u32(sV), kVRegion, 1024);
             const uint64_t pv_b0 = ptx::sdesc_sw128(ptx::smem_u32(sP), kPBytes, 1024);
             uint32_t ph = 0, sph = 0;
-            bool ok = true;
+            bool ok = true, seen = false;                // seen: the next block of V was found ready
             while (ok && walk.next(a, sg)) {
                 // the last segment's accumulators have been read (the first wait returns at once)
                 if (!ptx::mbar_wait(&S.o_free, sph ^ 1, abort_flag) || !ptx::mbar_wait(&S.q_full, sph, abort_flag)) break;
@@ -378,9 +403,12 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap vmap, const
                 for (int kt = sg.k0; kt < sg.k1; ++kt) {
 #pragma unroll
                     for (int mb = 0; mb < kBlocks; ++mb) {
-                        if (!ptx::mbar_wait(&S.v_full[mb], ph, abort_flag)) { ok = false; break; }
+                        if (!seen && !ptx::mbar_wait(&S.v_full[mb], ph, abort_flag)) { ok = false; break; }
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
+                            // the next block's barrier is polled while the tensor pipe has work: a wait takes
+                            // about 150 cycles even when it is over
+                            if (k == 7 && mb + 1 < kBlocks) seen = ptx::mbar_test(&S.v_full[(mb + 1) % kBlocks], ph);
                             const int rg = 2 * mb + (k >> 2);
                             ptx::mma_f16_ss(tmem, s_a0 + (uint64_t)(rg * (kVRegion >> 4) + (k & 3) * 2),
                                             s_b0 + (uint64_t)(rg * (kQRegion >> 4) + (k & 3) * 2), idesc_s, (mb | k) != 0);
@@ -390,15 +418,17 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap vmap, const
                     ptx::mma_commit(&S.s_full);
                     if (!ptx::mbar_wait(&S.p_full, ph, abort_flag)) { ok = false; break; }
                     ptx::tc_fence_after();
+                    ph ^= 1;
 #pragma unroll
                     for (int mb = 0; mb < kBlocks; ++mb) {
 #pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k)
+                        for (int k = 0; k < kTile / 16; ++k) {
+                            if (mb + 1 == kBlocks && k == 7) seen = ptx::mbar_test(&S.v_full[0], ph);
                             ptx::mma_f16_ss(tmem + kOCol + kQ * mb, pv_a0 + (uint64_t)(mb * (2 * kVRegion >> 4) + k * (2048 >> 4)),
                                             pv_b0 + (uint64_t)(k * (2048 >> 4)), idesc_pv, (kt > sg.k0 || k > 0) ? 1u : 0u);
+                        }
                         ptx::mma_commit(&S.v_empty[mb]);
                     }
-                    ph ^= 1;
                 }
                 if (ok) ptx::mma_commit(&S.seg_done);
             }
@@ -408,21 +438,23 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap vmap, const
         }
         __syncwarp();
     } else {
-        // ================= workers =================
-        const int sub = warp & 3, half = (warp - 2) >> 2;
-        const int wt = threadIdx.x - 64;
+        // ================= softmax and partials =================
+        // The four warps of a quarter (16 queries, all keys) work together, apart from the others.
+        const int sub = warp & 3, quarter = (warp - 2) >> 2;
+        const int c0 = quarter * kCols;
+        const int wt = (threadIdx.x - 64) & 127;         // thread of the quarter
+        const uint32_t bar = 1 + quarter;
         const int t = sub * 32 + lane;                   // key of the tile, and channel of a block
         const uint32_t lane_addr = tmem + ((uint32_t)(sub * 32) << 16);
-        const uint32_t s_addr = lane_addr + half * 32;
         uint32_t ph = 0, sph = 0;
         bool bad = false, aborted = false;
         while (!aborted && walk.next(a, sg)) {
             const uint8_t *valid = a.valid + (int64_t)sg.g * a.n_pad + t;
-            if (wt < kQ) S.zm[wt] = make_float2(a.qs[sg.tile * kQ + wt], -INFINITY);
-            ptx::named_barrier(1, kWorkers);
-            float l[32];
+            if (wt < kCols) S.zm[c0 + wt] = make_float2(a.qs[sg.tile * kQ + c0 + wt], -INFINITY);
+            ptx::named_barrier(bar, 128);
+            float l[kCols];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) l[i] = 0.0f;
+            for (int i = 0; i < kCols; ++i) l[i] = 0.0f;
             bool live_next = valid[(int64_t)sg.k0 * kTile] != 0;
             for (int kt = sg.k0; kt < sg.k1; ++kt) {
                 const bool live = live_next;
@@ -430,115 +462,108 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap vmap, const
                 if (!ptx::mbar_wait(&S.s_full, ph, abort_flag)) bad = true;
                 ph ^= 1;
                 ptx::tc_fence_after();
-                float z[32];
-                {
-                    uint32_t u[32];
-                    ptx::tmem_ld32(s_addr, u);
-                    ptx::tmem_ld_wait();
+                uint32_t u[kCols];
+                ptx::tmem_ld16(lane_addr + c0, u);
+                ptx::tmem_ld_wait();
+                // weights under the maxima so far, as the P^T line of this key; the first tile has none
+                // yet and goes on to the move below
+                float p[kCols];
+                auto weights = [&]() {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(u[i]);
-                }
+                    for (int c = 0; c < kCols / 8; ++c) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int i = 8 * c + 2 * k;
+                            const float4 zm = *reinterpret_cast<const float4 *>(&S.zm[c0 + i]);
+                            p[i] = live ? ptx::ex2(fmaf(__uint_as_float(u[i]), zm.x, -zm.y)) : 0.0f;
+                            p[i + 1] = live ? ptx::ex2(fmaf(__uint_as_float(u[i + 1]), zm.z, -zm.w)) : 0.0f;
+                            const __half2 h = __floats2half2_rn(p[i], p[i + 1]);
+                            w[k] = *reinterpret_cast<const uint32_t *>(&h);
+                        }
+                        *reinterpret_cast<uint4 *>(sP + tc::sw128_off(t, quarter * 2 + c)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                };
+                weights();
                 bool over = false;
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    const float4 c = *reinterpret_cast<const float4 *>(&S.zm[half * 32 + i]);
-                    z[i] *= c.x;
-                    z[i + 1] *= c.z;
-                    over |= (z[i] > c.y + (kShift + kLag)) | (z[i + 1] > c.w + (kShift + kLag));
-                }
+                for (int i = 0; i < kCols; ++i) over |= p[i] > kOver;
                 // one barrier decides whether to stop and whether some maximum moves
-                bool move = false;
-                if (tc::block_any((over && live) || bad || *abort_flag != 0, 1, kWorkers)) {
-                    if (tc::block_any(bad || *abort_flag != 0, 1, kWorkers)) { aborted = true; break; }
-                    move = true;
-                }
-                bool rescale = false;
-                if (move) {
-                    float v[32];
+                if (tc::block_any(over || bad || *abort_flag != 0, bar, 128)) {
+                    if (tc::block_any(bad || *abort_flag != 0, bar, 128)) { aborted = true; break; }
+                    float v[kCols];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = live ? z[i] : -INFINITY;
-                    tc::warp_transpose_reduce<false>(v, lane);
-                    S.red[sub][half * 32 + lane] = v[0];
-                    ptx::named_barrier(1, kWorkers);
+                    for (int i = 0; i < kCols; ++i) v[i] = live ? __uint_as_float(u[i]) * S.zm[c0 + i].x : -INFINITY;
+                    reduce16<false>(v, lane);
+                    if (lane < kCols) S.red[sub][c0 + lane] = v[0];
+                    ptx::named_barrier(bar, 128);
                     bool moved = false;
-                    if (wt < kQ) {
-                        const float top = fmaxf(fmaxf(S.red[0][wt], S.red[1][wt]), fmaxf(S.red[2][wt], S.red[3][wt]));
-                        const float old = S.zm[wt].y;    // maximum - kShift
+                    if (wt < kCols) {
+                        const int c = c0 + wt;
+                        const float top = fmaxf(fmaxf(S.red[0][c], S.red[1][c]), fmaxf(S.red[2][c], S.red[3][c]));
+                        const float old = S.zm[c].y;     // maximum - kShift
                         float al = 1.0f;
                         if (top > old + (kShift + kLag)) {
-                            S.zm[wt].y = top - kShift;
+                            S.zm[c].y = top - kShift;
                             al = old == -INFINITY ? 0.0f : ptx::ex2(old + kShift - top);
                             moved = kt > sg.k0 && old != -INFINITY;
                         }
-                        S.alpha[wt] = al;
+                        S.alpha[c] = al;
                     }
-                    rescale = tc::block_any(moved, 1, kWorkers);
+                    const bool rescale = tc::block_any(moved, bar, 128);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) l[i] *= S.alpha[half * 32 + i];
-                }
-                // weights, their sums, and the P^T line of this key
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int i = 8 * c + 2 * k;
-                        const float4 zm = *reinterpret_cast<const float4 *>(&S.zm[half * 32 + i]);
-                        const float p0 = live ? ptx::ex2(z[i] - zm.y) : 0.0f;
-                        const float p1 = live ? ptx::ex2(z[i + 1] - zm.w) : 0.0f;
-                        l[i] += p0;
-                        l[i + 1] += p1;
-                        const __half2 h = __floats2half2_rn(p0, p1);
-                        w[k] = *reinterpret_cast<const uint32_t *>(&h);
-                    }
-                    *reinterpret_cast<uint4 *>(sP + tc::sw128_off(t, half * 4 + c)) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-                // accumulators of queries whose maximum moved: S(kt) completed after the last tile's
-                // second product, so they are at rest
-                if (rescale) {
+                    for (int i = 0; i < kCols; ++i) l[i] *= S.alpha[c0 + i];
+                    weights();
+                    // accumulators of queries whose maximum moved: S(kt) completed after the last tile's
+                    // second product, so they are at rest
+                    if (rescale) {
 #pragma unroll 1
-                    for (int mb = 0; mb < kBlocks; ++mb) {
-                        uint32_t u[32];
-                        ptx::tmem_ld32(lane_addr + kOCol + kQ * mb + half * 32, u);
-                        ptx::tmem_ld_wait();
+                        for (int mb = 0; mb < kBlocks; ++mb) {
+                            uint32_t o[kCols];
+                            ptx::tmem_ld16(lane_addr + kOCol + kQ * mb + c0, o);
+                            ptx::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * S.alpha[half * 32 + i]);
-                        ptx::tmem_st32(lane_addr + kOCol + kQ * mb + half * 32, u);
+                            for (int i = 0; i < kCols; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * S.alpha[c0 + i]);
+                            ptx::tmem_st16(lane_addr + kOCol + kQ * mb + c0, o);
+                        }
+                        ptx::tmem_st_wait();
                     }
-                    ptx::tmem_st_wait();
                 }
                 ptx::fence_async_smem();
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&S.p_full);
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) l[i] += p[i];
             }
             if (aborted) break;
             // ---- the segment's partial ----
             if (!ptx::mbar_wait(&S.seg_done, sph, abort_flag)) bad = true;
             sph ^= 1;
-            if (tc::block_any(bad || *abort_flag != 0, 1, kWorkers)) { aborted = true; break; }
+            if (tc::block_any(bad || *abort_flag != 0, bar, 128)) { aborted = true; break; }
             ptx::tc_fence_after();
             float *part = a.parts + (blockIdx.x + sg.tile) * (int64_t)kPartFloats;
-            tc::warp_transpose_reduce<true>(l, lane);
-            S.red[sub][half * 32 + lane] = l[0];
-            ptx::named_barrier(1, kWorkers);
-            if (wt < kQ) {
-                part[wt] = S.zm[wt].y;
-                part[kQ + wt] = (S.red[0][wt] + S.red[1][wt]) + (S.red[2][wt] + S.red[3][wt]);
+            reduce16<true>(l, lane);
+            if (lane < kCols) S.red[sub][c0 + lane] = l[0];
+            ptx::named_barrier(bar, 128);
+            if (wt < kCols) {
+                const int c = c0 + wt;
+                part[c] = S.zm[c].y;
+                part[kQ + c] = (S.red[0][c] + S.red[1][c]) + (S.red[2][c] + S.red[3][c]);
             }
-#pragma unroll 1
-            for (int mb = 0; mb < kBlocks; ++mb) {
-                uint32_t u[32];
-                ptx::tmem_ld32(lane_addr + kOCol + kQ * mb + half * 32, u);
-                ptx::tmem_ld_wait();
-                float *o = part + 2 * kQ + (half * 32) * kLatent + mb * 128 + t;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i * kLatent] = __uint_as_float(u[i]);
+            for (int mb = 0; mb < kBlocks; ++mb) {
+                uint32_t o[kCols];
+                ptx::tmem_ld16(lane_addr + kOCol + kQ * mb + c0, o);
+                ptx::tmem_ld_wait();
+                float *dst = part + 2 * kQ + c0 * kLatent + mb * 128 + t;
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) dst[i * kLatent] = __uint_as_float(o[i]);
             }
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&S.o_free);
-            ptx::named_barrier(1, kWorkers);             // the shared maxima are read before they are reset
+            ptx::named_barrier(bar, 128);                // the shared maxima are read before they are reset
         }
     }
     ptx::tc_fence_before();
