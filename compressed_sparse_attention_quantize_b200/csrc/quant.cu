@@ -116,40 +116,95 @@ CSA2_D void load8(const T *x, bool vec, float (&v)[8]) {
     }
 }
 
+// x / s rounded to nearest, for finite x and r = RN(1/s): Markstein's step (IBM J. Res. Dev. 34(1),
+// 1990): q0 = RN(x r) is within one unit of x/s, x - q0 s is exact in one fma, and adding it times r
+// rounds the quotient correctly.  (Where q0 is subnormal the result is far below every code's reach.)
+CSA2_D float quotient_rn(float x, float s, float r) {
+    const float q0 = x * r;
+    return __fmaf_rn(__fmaf_rn(-q0, s, x), r, q0);
+}
+// E2M1 codes of 8 values, value k in bits 4k..: nearest, ties to even, saturating at 6, the sign kept.
+CSA2_D uint32_t e2m1_codes8(const float (&v)[8]) {
+    uint32_t w;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(w)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return w;
+}
+// E4M3 code of a finite a >= 0 (nearest-even, satfinite), and its value.
+CSA2_D uint32_t e4m3_code_hw(float a) {
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.0f), "f"(a));
+    return c & 0xFFu;
+}
+CSA2_D float e4m3_value_hw(uint32_t code) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)code));
+    return __low2float(*reinterpret_cast<const __half2 *>(&h));
+}
+
 // The codes of 8 neighbouring channels (channel k in bits 4k..) and their block's scale byte; the
-// block's 2 (E4M3 / 16 channels) or 4 (E8M0 / 32 channels) lanes call together.
+// block's 2 (E4M3 / 16 channels) or 4 (E8M0 / 32 channels) lanes call together.  The conversions take
+// the exact scaled value (E8M0: times a power of two) or the correctly rounded quotient (E4M3: a
+// scale has at most 4 significant bits, so a quotient that is not exact lies more than half an fp32
+// ulp from every E2M1 midpoint, and amax / 6 from every E4M3 one).  Blocks with an infinity or a NaN
+// take the comparisons.
 template <int FMT>
 CSA2_D uint32_t quantize_lane8(const float (&v)[8], uint32_t &scale) {
     uint32_t top = 0u;                                   // |x| as bits: ordered, and NaN above all
 #pragma unroll
     for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[k]) & 0x7FFFFFFFu);
-    float s;
+    float y[8];
     if (FMT == CSA2_FMT_MXFP4_E2M1_E8M0S32) {
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         scale = e8m0_scale_byte(top);
-        s = scale == 255u ? 0.0f : e8m0_to_f32(scale);
-    } else {
+        if (scale == 255u) return 0u;
+        const float inv = __uint_as_float((254u - scale) << 23);      // 2^(127 - byte), byte <= 252
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = v[k] * inv;
+        return e2m1_codes8(y);
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    if (top >= 0x7F800000u) {
         // as fmaxf over the block: a NaN takes no part
         float amax = 0.0f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(v[k]));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        // (both lanes of the block are here)
+        const uint32_t pair = 3u << ((threadIdx.x & 31u) & ~1u);
+        amax = fmaxf(amax, __shfl_xor_sync(pair, amax, 1));
         scale = e4m3_code_mag_rne(__fdiv_rn(amax, 6.0f));
-        s = e4m3_to_f32(scale);
-    }
-    uint32_t w = 0u;
-    if (s != 0.0f) {
-        const E2M1Cuts t = e2m1_cuts(s);
+        const float s = e4m3_to_f32(scale);
+        uint32_t w = 0u;
+        if (s != 0.0f) {
+            const E2M1Cuts t = e2m1_cuts(s);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w |= e2m1_code(v[k], t) << (4 * k);
+            for (int k = 0; k < 8; ++k) w |= e2m1_code(v[k], t) << (4 * k);
+        }
+        return w;
     }
-    return w;
+    scale = e4m3_code_hw(quotient_rn(__uint_as_float(top), 6.0f, 1.0f / 6.0f));
+    if (scale == 0u) return 0u;
+    const float s = e4m3_value_hw(scale), r = __frcp_rn(s);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = quotient_rn(v[k], s, r);
+    return e2m1_codes8(y);
 }
 
-// FP4 rows: 8 neighbouring channels per thread, read in 16-byte loads where the rows allow it.
-// Bound by memory: x is read once and 4.25 or 4.5 bits per channel are written.
-template <typename T, int FMT>
+// FP4 rows: 8 neighbouring channels per piece, read in 16-byte loads where the rows allow it; a thread
+// takes kPieces pieces a block's width apart, all loads issued before the first is used.  Bound by
+// memory: x is read once and 4.25 or 4.5 bits per channel are written.  kDense: rows, codes and scales
+// without gaps and in place order, so that piece t is at 8 t: no division by the row length.
+// Measured at 4096 rows of 4096 bf16 channels (E4M3 / E8M0 scales): one piece a thread with the rows'
+// division and the comparisons per code 25.9 / 24.9 us; conversions 16.1 / 13.6 us.
+constexpr int kPieces = 4;
+template <typename T, int FMT, bool kDense>
 __global__ void __launch_bounds__(256)
 quant_fp4_rows_kernel(const T *__restrict__ x, int64_t rows, int dim, int64_t x_stride,
                       uint8_t *__restrict__ codes, int64_t code_stride, uint8_t *__restrict__ scales,
@@ -157,35 +212,48 @@ quant_fp4_rows_kernel(const T *__restrict__ x, int64_t rows, int dim, int64_t x_
     constexpr int kLanes = FMT == CSA2_FMT_MXFP4_E2M1_E8M0S32 ? 4 : 2;   // lanes of a block
     const uint32_t per_row = (uint32_t)dim >> 3;
     const int64_t total = rows * (int64_t)per_row;
-    for (int64_t base = (int64_t)blockIdx.x * 256; base < total; base += (int64_t)gridDim.x * 256) {
-        const int64_t t = base + threadIdx.x;
-        const bool live = t < total;                     // blocks are whole: total is a multiple of kLanes
-        float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        int64_t d = -1;
-        uint32_t c = 0;
-        if (live) {
-            int64_t r;
-            if (total <= 0xFFFFFFFFll) {                 // a 32-bit division where it suffices
-                r = (uint32_t)t / per_row;
-                c = (uint32_t)t - (uint32_t)r * per_row;
-            } else {
-                r = t / per_row;
-                c = (uint32_t)(t - r * per_row);
+    for (int64_t base = (int64_t)blockIdx.x * (256 * kPieces); base < total; base += (int64_t)gridDim.x * (256 * kPieces)) {
+        float v[kPieces][8];
+        int64_t d[kPieces], at[kPieces];                 // destination row (-1: none), piece of the row
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            const int64_t t = base + 256 * j + threadIdx.x;
+            d[j] = -1;
+            at[j] = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[j][k] = 0.0f;
+            if (t < total) {                             // blocks are whole: total is a multiple of kLanes
+                if (kDense) {
+                    d[j] = 0;
+                    at[j] = t;
+                    load8<T>(x + 8 * t, true, v[j]);
+                } else {
+                    int64_t r;
+                    if (total <= 0xFFFFFFFFll) {         // a 32-bit division where it suffices
+                        r = (uint32_t)t / per_row;
+                        at[j] = (uint32_t)t - (uint32_t)r * per_row;
+                    } else {
+                        r = t / per_row;
+                        at[j] = t - r * per_row;
+                    }
+                    load8<T>(x + r * x_stride + 8 * at[j], vec, v[j]);
+                    d[j] = dst_rows ? dst_rows[r] : r;
+                }
             }
-            load8<T>(x + r * x_stride + 8 * (int64_t)c, vec, v);
-            d = dst_rows ? dst_rows[r] : r;
         }
-        uint32_t sc;
-        const uint32_t w = quantize_lane8<FMT>(v, sc);
-        if (d >= 0) {
-            uint8_t *cd = codes + d * code_stride + 4 * (int64_t)c;
-            if (word) {
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            uint32_t sc;
+            const uint32_t w = quantize_lane8<FMT>(v[j], sc);
+            if (d[j] < 0) continue;
+            uint8_t *cd = codes + d[j] * code_stride + 4 * at[j];
+            if (kDense || word) {
                 *reinterpret_cast<uint32_t *>(cd) = w;
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) cd[k] = (uint8_t)(w >> (8 * k));
             }
-            if (c % kLanes == 0) scales[d * scale_stride + c / kLanes] = (uint8_t)sc;
+            if (at[j] % kLanes == 0) scales[d[j] * scale_stride + at[j] / kLanes] = (uint8_t)sc;
         }
     }
 }
@@ -541,9 +609,15 @@ static void launch_quant_fp4_rows(const T *x, int64_t rows, int dim, int64_t x_s
                                   const int64_t *dst_rows, cudaStream_t st) {
     const bool vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (x_stride * (int64_t)sizeof(T)) % 16 == 0;
     const bool word = ((reinterpret_cast<uintptr_t>(codes) | (uintptr_t)code_stride) & 3u) == 0;
-    const int64_t blocks = std::min<int64_t>(ceil_div(rows * (dim / 8), 256), 148 * 64);
-    quant_fp4_rows_kernel<T, FMT><<<(unsigned)blocks, 256, 0, st>>>(x, rows, dim, x_stride, codes, code_stride, scales,
-                                                                    scale_stride, dst_rows, vec, word);
+    const int lanes = FMT == CSA2_FMT_MXFP4_E2M1_E8M0S32 ? 32 : 16;
+    const bool dense = vec && word && !dst_rows && x_stride == dim && code_stride == dim / 2 && scale_stride == dim / lanes;
+    const int64_t blocks = std::min<int64_t>(ceil_div(rows * (dim / 8), 256 * kPieces), 148 * 64);
+    if (dense)
+        quant_fp4_rows_kernel<T, FMT, true><<<(unsigned)blocks, 256, 0, st>>>(x, rows, dim, x_stride, codes, code_stride,
+                                                                              scales, scale_stride, dst_rows, vec, word);
+    else
+        quant_fp4_rows_kernel<T, FMT, false><<<(unsigned)blocks, 256, 0, st>>>(x, rows, dim, x_stride, codes, code_stride,
+                                                                               scales, scale_stride, dst_rows, vec, word);
 }
 
 cudaError_t launch_quant_fp4(int fmt, const void *x, int x_dtype, int64_t rows, int dim, int64_t x_stride,
