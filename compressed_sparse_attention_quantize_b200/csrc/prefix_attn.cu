@@ -13,25 +13,38 @@
 //     padded array of the workspace, through the block table; the queries to fp16, each row times
 //     a power of two that puts its largest element in [2^13, 2^14) (exact for all elements within
 //     2^27 of it, and a row of infinities or NaNs spoils no other); the groups' tile counts.
-//  2. prefix_attn_kernel  a persistent CTA per SM.  The work is the list of (64 queries, 128 keys)
-//     tiles, all key tiles of one query tile after the other; CTA i takes the i-th equal share, so
-//     every SM has the same number of tiles, and a query tile is cut at most where shares meet.
-//     Each piece leaves a partial (maxima, sums, fp32 output).
+//  2. prefix_attn_kernel  a persistent pair of CTAs per SM pair.  The work is the list of (128 queries,
+//     128 keys) tiles, all key tiles of one query tile after the other; pair i takes the i-th equal
+//     share, so every pair has the same number of tiles, and a query tile is cut at most where shares
+//     meet.  Each piece leaves a partial (maxima, sums, fp32 output) per 64 queries.
 //  3. prefix_merge_kernel  partials of a query in share order, then the own part: a fixed order.
 //
-// Tile arithmetic, as in csa2_sparse_attn's kernel, with the entries already fp16:
-//   S^T[key, query] = V . Q^T     M=128 keys, N=64 queries, K=512: A = V (K-major), B = Q (K-major)
-//   softmax                       16 warps: one key per thread, 16 queries; running maxima that move
-//                                 only when some logit exceeds them by 2^8; sums of the unrounded fp32
-//                                 weights, per key in registers until the end
-//   O^T[chan, query] += V^T.P^T   four blocks of M=128 channels, N=64, K=128 keys: the same V bytes
+// Tile arithmetic (tcgen05.mma cta_group::2, M = 128 queries, 64 of each CTA):
+//   S[query, key] = Q . V^T     N=128 keys, K=512 channels: each CTA holds its own 64 queries and
+//                               64 of the keys; S of its queries lands in its TMEM (lanes 0-63: keys
+//                               0-63, lanes 64-127: keys 64-127; 64 columns, two buffers)
+//   softmax                     8 warps: a thread has one query and 32 keys; the running maximum
+//                               moves only when some logit exceeds it by 2^8; sums of the unrounded
+//                               fp32 weights in registers
+//   O[query, chan] += P . V     two MMAs of N=256 channels, K=128 keys: each CTA holds 128 channels
+//                               of every key for each, read MN-major (lanes 0-63: its lower, 64-127:
+//                               the upper 128 channels; 2 x 128 columns)
+// With 64 queries per CTA the 512-wide accumulators take half of TMEM, which one CTA of 128 queries
+// could not hold next to S; both products read the latent from the two CTAs' shared memory, half
+// each.  S of the next tile runs under the softmax of this one: K and V come separately, in two halves
+// of the channels each, refilled as soon as their MMAs are done.
 // P is rounded to fp16 with the weights scaled to at most 2^15 (the maximum itself to 2^7), so weights
 // down to 2^-21 of the maximum keep 11 bits and the rest an absolute 2^-32: the rounding is at most
-// 2^-12 of sum_j p_j |v_j| / sum_j p_j plus n 2^-32 max |v|.
+// 2^-11 of sum_j p_j |v_j| / sum_j p_j plus n 2^-32 max |v|.
 //
-// Bound: the tensor pipe at N=64, where the A operand's shared-memory reads cap it at 67% (48 cycles
-// per M=128, N=64, K=16 MMA), plus the softmax between a tile's two products, which one V buffer of
-// 128 KB cannot overlap.  Channel blocks of V are refilled one by one as the second product frees them.
+// Roles per CTA: warp 0 copies Q and K, warp 1 copies V; warps 2 and 3 issue the MMAs of S and of O
+// (first CTA) or pass the arrival of the second CTA's copies on to the first; warps 4-11 softmax and
+// partials.
+//
+// Bound: MMAs of N=128 take 46 cycles and N=256 60 (measured), 2432 a tile, and the tile's
+// shared-memory traffic (operands 224 KB, copies 128 KB, P 16 KB) 2900 cycles at 128 bytes a cycle.
+// One CTA per 64 queries with S^T = V . Q^T (N=64, one 128 KB V buffer for both products, so that the
+// softmax lay between them) took 6400 cycles a tile: 825 us for 128 rows x 64 heads on 32768 entries.
 // Every wait is bounded: on expiry the CTA records CSA2_ERR_TIMEOUT, drains, frees TMEM and exits.
 #include "common.cuh"
 #include "tc_ptx.cuh"
@@ -39,24 +52,29 @@
 namespace csa2 {
 namespace pfx {
 
-constexpr int kQ = 64;                     // queries per tile (MMA N)
-constexpr int kTile = 128;                 // keys per tile (MMA M)
-constexpr int kBlocks = 4;                 // 128-channel blocks
+constexpr int kQ = 128;                    // queries per tile
+constexpr int kQHalf = 64;                 // of each CTA
+constexpr int kTile = 128;                 // keys per tile
+constexpr int kKeyHalf = 64;               // K rows of each CTA
 constexpr int kRegion = 64;                // channels of a 128-byte swizzled row
-constexpr int kQRegion = kQ * 128;         // 8 KB
+constexpr int kQRegion = kQHalf * 128;     // 8 KB
+constexpr int kKRegion = kKeyHalf * 128;   // 8 KB
 constexpr int kVRegion = kTile * 128;      // 16 KB
+constexpr int kKSlots = 2;                 // of 256 channels: 4 regions
+constexpr int kKSlot = 4 * kKRegion;
+constexpr int kVSlot = 2 * kVRegion;       // 128 channels, the CTA's half of an N=256 MMA
 constexpr int kQBytes = 8 * kQRegion;
-constexpr int kVBytes = 8 * kVRegion;
-constexpr int kPBytes = kTile * kQ * 2;
-constexpr int kThreads = 576;              // copies, MMA issuer, 16 softmax warps
-constexpr int kWorkerWarps = 16;
-constexpr int kCols = 16;                  // queries per softmax warp
+constexpr int kPBytes = kQHalf * kTile * 2;
+constexpr int kThreads = 384;
+constexpr int kSoftWarp0 = 4;
+constexpr int kSoftWarps = 8;
 constexpr int kTmemCols = 512;
-constexpr int kOCol = 128;                 // O^T accumulators; S^T at column 0
+constexpr int kSCols = 64;                 // a buffer of S; two from column 0
+constexpr int kOCol = 128;                 // two accumulators of 128 columns
 constexpr float kShift = 7.0f;             // log2 of the weight of the running maximum
 constexpr float kLag = 8.0f;               // log2 units a logit may exceed the running maximum by
 constexpr float kOver = 32768.0f;          // a weight above 2^(kShift + kLag): the maximum moves
-constexpr int kPartFloats = 2 * kQ + kQ * kLatent;
+constexpr int kPartFloats = 2 * kQHalf + kQHalf * kLatent;
 
 // Per group, in the workspace (written by the first launch): first query row, first query tile and
 // first work item; entry [G] holds the totals.
@@ -87,11 +105,11 @@ struct Args {
     Group *groups;                         // [G + 1]
     __half *v;                             // [G][n_pad][512]
     uint8_t *valid;                        // [G][n_pad]
-    __half *qh;                            // [tiles][64][512]
-    float *qs;                             // [tiles][64]: logit per unit of S
-    float *parts;                          // [CTAs + tiles][kPartFloats]
+    __half *qh;                            // [tiles][128][512]
+    float *qs;                             // [tiles][128]: logit per unit of S
+    float *parts;                          // [pairs + tiles][2][kPartFloats]
     int64_t max_tiles;
-    int ctas;
+    int pairs;
 };
 
 // ---------------------------------------------------------------------------------------------
@@ -247,39 +265,16 @@ __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(const Args a)
 // 2. tiles
 // ---------------------------------------------------------------------------------------------
 struct Ctl {
-    uint64_t v_full[kBlocks], v_empty[kBlocks];
-    uint64_t q_full, s_full, p_full, seg_done, o_free, drain;
+    uint64_t k_full[kKSlots], k_empty[kKSlots], v_full[2], v_empty[2];
+    uint64_t q_full, q_empty, s_full[2], s_free[2], p_full, seg_done, o_free, drain;
     uint32_t tmem_base;
     int abort_flag;
-    alignas(16) float2 zm[kQ];             // (read in 16-byte pieces) logit per unit of S, running maximum - kShift
-    float alpha[kQ];
-    float red[4][kQ];
+    float red[4][kQHalf];
 };
-constexpr int kSmemBytes = kQBytes + kVBytes + kPBytes + (int)sizeof(Ctl) + 1024;
+constexpr int kSmemBytes = kQBytes + kKSlots * kKSlot + 2 * kVSlot + kPBytes + (int)sizeof(Ctl) + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
 
-// Reduce 16 values over a warp's lanes: afterwards v[0] of lanes c and c + 16 holds the maximum (or sum)
-// of element c.
-template <bool kSum>
-CSA2_D void reduce16(float (&v)[kCols], int lane) {
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) {
-        const float o = __shfl_xor_sync(0xffffffffu, v[i], 16);
-        v[i] = kSum ? v[i] + o : fmaxf(v[i], o);
-    }
-#pragma unroll
-    for (int off = 8, n = 8; off >= 1; off >>= 1, n >>= 1) {
-        const bool upper = (lane & off) != 0;
-#pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const float send = upper ? v[i] : v[i + n];
-            const float keep = upper ? v[i + n] : v[i];
-            const float got = __shfl_xor_sync(0xffffffffu, send, off);
-            v[i] = kSum ? keep + got : fmaxf(keep, got);
-        }
-    }
-}
-
-// A run of key tiles of one query tile: what a CTA does between two changes of Q.
+// A run of key tiles of one query tile: what a pair does between two changes of Q.
 struct Segment {
     int64_t tile;                          // query tile
     int g;
@@ -303,238 +298,369 @@ struct Walk {
         return true;
     }
 };
-// The CTAs that get a share: no share is empty.
-CSA2_D int64_t shares_of(const Args &a, int64_t total) { return min((int64_t)a.ctas, total); }
-CSA2_D Walk walk_of(const Args &a, int cta) {
+// The pairs that get a share: no share is empty.
+CSA2_D int64_t shares_of(const Args &a, int64_t total) { return min((int64_t)a.pairs, total); }
+CSA2_D Walk walk_of(const Args &a, int pair) {
     const int64_t total = a.groups[a.G].work0, shares = shares_of(a, total);
-    if (cta >= shares) return {0, 0};
-    return {total * cta / shares, total * (cta + 1) / shares};
+    if (pair >= shares) return {0, 0};
+    return {total * pair / shares, total * (pair + 1) / shares};
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
-prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap) {
+// A place in a ring of n slots and the parity of its round.
+template <int n>
+struct Ring {
+    int st = 0;
+    uint32_t ph = 0;
+    CSA2_D void next() {
+        if (++st == n) {
+            st = 0;
+            ph ^= 1;
+        }
+    }
+};
+
+CSA2_D void mma2_f16_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+// Arrives once on `bar` of both CTAs when every MMA issued so far by this thread has completed.
+CSA2_D void commit2(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(ptx::smem_u32(bar)), "h"((uint16_t)3) : "memory");
+}
+// On the first CTA's copy of `bar`.  What an arrival hands over is read by the tensor core of the
+// arriving thread's own SM (operands in its shared memory, behind a proxy fence or a completed copy;
+// its TMEM, behind a tcgen05 fence), so the barriers keep their default scope: with .release.cluster
+// and .acquire.cluster an arrival took 1250 cycles and a wait that was over 450, and the kernel 40%
+// longer than one CTA per 64 queries.
+CSA2_D void arrive_first(uint64_t *bar) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(ptx::smem_u32(bar)));
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
+}
+CSA2_D void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Which of 32 keys count: their 32 bytes (0 or 1) as a bit mask.
+CSA2_D uint32_t key_mask(const uint4 &a, const uint4 &b) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m |= ((w[i] * 0x01020408u >> 24) & 15u) << (4 * i);
+    return m;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                   const __grid_constant__ CUtensorMap qmap) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint8_t *sQ = base, *sV = sQ + kQBytes, *sP = sV + kVBytes;
+    uint8_t *sQ = base, *sK = sQ + kQBytes, *sV = sK + kKSlots * kKSlot, *sP = sV + 2 * kVSlot;
     Ctl &S = *reinterpret_cast<Ctl *>(sP + kPBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Walk walk = walk_of(a, blockIdx.x);
-    if (walk.u >= walk.end) return;                      // uniform: nothing allocated yet
+    const int rank = (int)(blockIdx.x & 1), pair = (int)(blockIdx.x >> 1);
+    Walk walk = walk_of(a, pair);
+    if (walk.u >= walk.end) return;                      // both CTAs of the pair: nothing allocated yet
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kBlocks; ++i) {
-            ptx::mbar_init(&S.v_full[i], 1);
-            ptx::mbar_init(&S.v_empty[i], 1);
+        // the first CTA's "full" barriers also count the second CTA's copies
+        for (int i = 0; i < kKSlots; ++i) {
+            ptx::mbar_init(&S.k_full[i], rank == 0 ? 2 : 1);
+            ptx::mbar_init(&S.k_empty[i], 1);
         }
-        ptx::mbar_init(&S.q_full, 1);
-        ptx::mbar_init(&S.s_full, 1);
-        ptx::mbar_init(&S.p_full, kWorkerWarps);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&S.v_full[i], rank == 0 ? 2 : 1);
+            ptx::mbar_init(&S.v_empty[i], 1);
+            ptx::mbar_init(&S.s_full[i], 1);
+            ptx::mbar_init(&S.s_free[i], 2 * kSoftWarps);
+        }
+        ptx::mbar_init(&S.q_full, rank == 0 ? 2 : 1);
+        ptx::mbar_init(&S.q_empty, 1);
+        ptx::mbar_init(&S.p_full, 2 * kSoftWarps);
         ptx::mbar_init(&S.seg_done, 1);
-        ptx::mbar_init(&S.o_free, kWorkerWarps);
-        ptx::mbar_init(&S.drain, 1);
+        ptx::mbar_init(&S.o_free, 2 * kSoftWarps);
+        ptx::mbar_init(&S.drain, 2);
         S.abort_flag = 0;
         ptx::fence_async_smem();
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 1) {
-        ptx::tmem_alloc(&S.tmem_base, kTmemCols);
-        ptx::tmem_relinquish();
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(ptx::smem_u32(&S.tmem_base)), "r"((uint32_t)kTmemCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
     ptx::tc_fence_before();
     __syncthreads();
+    cluster_sync();
     ptx::tc_fence_after();
     const uint32_t tmem = S.tmem_base;
     volatile int *abort_flag = &S.abort_flag;
     Segment sg;
 
     if (warp == 0) {
-        // ================= copies =================
+        // ================= copies of Q and K =================
         if (lane == 0) {
-            uint32_t sph = 1, vph = 1;                   // parities: the last segment's end, V's last release
-            int uses[kBlocks] = {0, 0, 0, 0}, q_uses = 0;
+            Ring<kKSlots> kr;
+            uint32_t sph = 1;                            // parity of Q's last release
+            int used = 0, q_uses = 0;
             bool ok = true;
             while (ok && walk.next(a, sg)) {
-                const int32_t y0 = (int32_t)((int64_t)sg.g * a.n_pad);
+                const int32_t y0 = (int32_t)((int64_t)sg.g * a.n_pad) + rank * kKeyHalf;
                 for (int kt = sg.k0; ok && kt < sg.k1; ++kt) {
-#pragma unroll
-                    for (int mb = 0; mb < kBlocks; ++mb) {
-                        if (!ok || !ptx::mbar_wait(&S.v_empty[mb], vph, abort_flag)) { ok = false; continue; }
-                        ++uses[mb];
-                        uint8_t *dst = sV + 2 * mb * kVRegion;
-                        ptx::mbar_arrive_expect_tx(&S.v_full[mb], 2 * kVRegion);
-                        ptx::tma_load_2d(dst, &vmap, 128 * mb, y0 + kt * kTile, &S.v_full[mb]);
-                        ptx::tma_load_2d(dst + kVRegion, &vmap, 128 * mb + kRegion, y0 + kt * kTile, &S.v_full[mb]);
-                    }
-                    if (!ok) break;
-                    vph ^= 1;
-                    if (kt == sg.k0) {                   // Q once the last segment's products are done
-                        if (!ptx::mbar_wait(&S.seg_done, sph, abort_flag)) { ok = false; break; }
-                        sph ^= 1;
-                        ptx::mbar_arrive_expect_tx(&S.q_full, kQBytes);
-                        for (int r = 0; r < 8; ++r)
-                            ptx::tma_load_2d(sQ + r * kQRegion, &qmap, r * kRegion, (int32_t)(sg.tile * kQ), &S.q_full);
-                        ++q_uses;
+                    for (int h = 0; h < kKSlots; ++h) {
+                        if (!ptx::mbar_wait(&S.k_empty[kr.st], kr.ph ^ 1, abort_flag)) { ok = false; break; }
+                        uint8_t *dst = sK + kr.st * kKSlot;
+                        ptx::mbar_arrive_expect_tx(&S.k_full[kr.st], kKSlot);
+                        for (int r = 0; r < 4; ++r)
+                            ptx::tma_load_2d(dst + r * kKRegion, &kmap, 256 * h + kRegion * r, y0 + kt * kTile, &S.k_full[kr.st]);
+                        kr.next();
+                        used = min(used + 1, kKSlots);
+                        if (kt == sg.k0 && h == 0) {     // Q once the last segment's scores are done
+                            if (!ptx::mbar_wait(&S.q_empty, sph, abort_flag)) { ok = false; break; }
+                            sph ^= 1;
+                            ptx::mbar_arrive_expect_tx(&S.q_full, kQBytes);
+                            for (int r = 0; r < 8; ++r)
+                                ptx::tma_load_2d(sQ + r * kQRegion, &qmap, r * kRegion,
+                                                 (int32_t)(sg.tile * kQ) + rank * kQHalf, &S.q_full);
+                            ++q_uses;
+                        }
                     }
                 }
             }
             // copies in flight land before the CTA leaves (already so unless it gave up early)
-#pragma unroll
-            for (int mb = 0; mb < kBlocks; ++mb)
-                if (uses[mb] > 0) ptx::mbar_wait_drain(&S.v_full[mb], (uses[mb] - 1) & 1);
+            for (; used > 0; --used) {
+                if (kr.st == 0) { kr.st = kKSlots; kr.ph ^= 1; }
+                --kr.st;
+                ptx::mbar_wait_drain(&S.k_full[kr.st], kr.ph);
+            }
             if (q_uses > 0) ptx::mbar_wait_drain(&S.q_full, (q_uses - 1) & 1);
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ================= MMA issuer =================
+        // ================= copies of V =================
         if (lane == 0) {
-            constexpr uint32_t idesc_s = ptx::idesc_f16_f32(128, kQ, false, false);
-            constexpr uint32_t idesc_pv = ptx::idesc_f16_f32(128, kQ, true, true);
-            const uint64_t s_a0 = ptx::sdesc_sw128(ptx::smem_u32(sV), 16, 1024);
-            const uint64_t s_b0 = ptx::sdesc_sw128(ptx::smem_u32(sQ), 16, 1024);
-            // V read MN-major: 64 channels per 128-byte row, the next 64 one region further; P likewise
-            const uint64_t pv_a0 = ptx::sdesc_sw128(ptx::smem_u32(sV), kVRegion, 1024);
-            const uint64_t pv_b0 = ptx::sdesc_sw128(ptx::smem_u32(sP), kPBytes, 1024);
-            uint32_t ph = 0, sph = 0;
-            bool ok = true, seen = false;                // seen: the next block of V was found ready
+            Ring<2> vr;
+            int used = 0;
+            bool ok = true;
             while (ok && walk.next(a, sg)) {
-                // the last segment's accumulators have been read (the first wait returns at once)
-                if (!ptx::mbar_wait(&S.o_free, sph ^ 1, abort_flag) || !ptx::mbar_wait(&S.q_full, sph, abort_flag)) break;
-                sph ^= 1;
-                ptx::tc_fence_after();
-                for (int kt = sg.k0; kt < sg.k1; ++kt) {
-#pragma unroll
-                    for (int mb = 0; mb < kBlocks; ++mb) {
-                        if (!seen && !ptx::mbar_wait(&S.v_full[mb], ph, abort_flag)) { ok = false; break; }
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            // the next block's barrier is polled while the tensor pipe has work: a wait takes
-                            // about 150 cycles even when it is over
-                            if (k == 7 && mb + 1 < kBlocks) seen = ptx::mbar_test(&S.v_full[(mb + 1) % kBlocks], ph);
-                            const int rg = 2 * mb + (k >> 2);
-                            ptx::mma_f16_ss(tmem, s_a0 + (uint64_t)(rg * (kVRegion >> 4) + (k & 3) * 2),
-                                            s_b0 + (uint64_t)(rg * (kQRegion >> 4) + (k & 3) * 2), idesc_s, (mb | k) != 0);
-                        }
+                const int32_t y0 = (int32_t)((int64_t)sg.g * a.n_pad);
+                for (int kt = sg.k0; ok && kt < sg.k1; ++kt)
+                    for (int i = 0; i < 2; ++i) {
+                        if (!ptx::mbar_wait(&S.v_empty[vr.st], vr.ph ^ 1, abort_flag)) { ok = false; break; }
+                        uint8_t *dst = sV + vr.st * kVSlot;
+                        const int32_t x = 256 * i + 128 * rank;
+                        ptx::mbar_arrive_expect_tx(&S.v_full[vr.st], kVSlot);
+                        ptx::tma_load_2d(dst, &vmap, x, y0 + kt * kTile, &S.v_full[vr.st]);
+                        ptx::tma_load_2d(dst + kVRegion, &vmap, x + kRegion, y0 + kt * kTile, &S.v_full[vr.st]);
+                        vr.next();
+                        used = min(used + 1, 2);
                     }
-                    if (!ok) break;
-                    ptx::mma_commit(&S.s_full);
-                    if (!ptx::mbar_wait(&S.p_full, ph, abort_flag)) { ok = false; break; }
-                    ptx::tc_fence_after();
-                    ph ^= 1;
-#pragma unroll
-                    for (int mb = 0; mb < kBlocks; ++mb) {
-#pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k) {
-                            if (mb + 1 == kBlocks && k == 7) seen = ptx::mbar_test(&S.v_full[0], ph);
-                            ptx::mma_f16_ss(tmem + kOCol + kQ * mb, pv_a0 + (uint64_t)(mb * (2 * kVRegion >> 4) + k * (2048 >> 4)),
-                                            pv_b0 + (uint64_t)(k * (2048 >> 4)), idesc_pv, (kt > sg.k0 || k > 0) ? 1u : 0u);
-                        }
-                        ptx::mma_commit(&S.v_empty[mb]);
-                    }
-                }
-                if (ok) ptx::mma_commit(&S.seg_done);
             }
-            // every issued MMA has completed before TMEM is released
-            ptx::mma_commit(&S.drain);
-            ptx::mbar_wait_drain(&S.drain, 0);
+            for (; used > 0; --used) {
+                if (vr.st == 0) { vr.st = 2; vr.ph ^= 1; }
+                --vr.st;
+                ptx::mbar_wait_drain(&S.v_full[vr.st], vr.ph);
+            }
         }
         __syncwarp();
-    } else {
+    } else if (warp == 2) {
+        Ring<kKSlots> kr;
+        uint32_t sph = 0;
+        bool ok = true;
+        if (lane == 0 && rank == 0) {
+            // ================= scores: S = Q . V^T =================
+            constexpr uint32_t idesc = ptx::idesc_f16_f32(128, kTile, false, false);
+            const uint64_t q0 = ptx::sdesc_sw128(ptx::smem_u32(sQ), 16, 1024);
+            const uint64_t k0 = ptx::sdesc_sw128(ptx::smem_u32(sK), 16, 1024);
+            Ring<2> sb;
+            while (ok && walk.next(a, sg)) {
+                if (!ptx::mbar_wait(&S.q_full, sph, abort_flag)) break;
+                sph ^= 1;
+                for (int kt = sg.k0; ok && kt < sg.k1; ++kt) {
+                    // the softmax has read this buffer's last scores
+                    if (!ptx::mbar_wait(&S.s_free[sb.st], sb.ph ^ 1, abort_flag)) { ok = false; break; }
+                    ptx::tc_fence_after();
+#pragma unroll
+                    for (int h = 0; h < kKSlots; ++h) {
+                        if (!ptx::mbar_wait(&S.k_full[h], kr.ph, abort_flag)) { ok = false; break; }
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            mma2_f16_ss(tmem + sb.st * kSCols, q0 + (uint64_t)((4 * h + (k >> 2)) * (kQRegion >> 4) + (k & 3) * 2),
+                                        k0 + (uint64_t)(h * (kKSlot >> 4) + (k >> 2) * (kKRegion >> 4) + (k & 3) * 2), idesc,
+                                        (h | k) != 0);
+                        commit2(&S.k_empty[h]);
+                    }
+                    if (!ok) break;
+                    kr.ph ^= 1;
+                    commit2(&S.s_full[sb.st]);
+                    sb.next();
+                }
+                if (ok) commit2(&S.q_empty);
+            }
+            // every issued MMA has completed before TMEM is released
+            commit2(&S.drain);
+            ptx::mbar_wait_drain(&S.drain, 0);
+        } else if (lane == 0) {
+            // ================= the second CTA's copies of Q and K, passed on =================
+            while (ok && walk.next(a, sg)) {
+                ok = ptx::mbar_wait(&S.q_full, sph, abort_flag);
+                sph ^= 1;
+                if (ok) arrive_first(&S.q_full);
+                for (int kt = sg.k0; ok && kt < sg.k1; ++kt)
+                    for (int h = 0; h < kKSlots && ok; ++h, kr.next()) {
+                        ok = ptx::mbar_wait(&S.k_full[kr.st], kr.ph, abort_flag);
+                        if (ok) arrive_first(&S.k_full[kr.st]);
+                    }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 3) {
+        uint32_t ph = 0, sph = 1;                        // tiles; the last segment's accumulators
+        bool ok = true;
+        if (lane == 0 && rank == 0) {
+            // ================= output: O += P . V =================
+            // A thread of its own: its waits and commits (150 and 60 cycles each, during which a thread's
+            // MMAs stand still) run under the scores' MMAs, and the other way round.
+            constexpr uint32_t idesc = ptx::idesc_f16_f32(128, 256, false, true);
+            const uint64_t p0 = ptx::sdesc_sw128(ptx::smem_u32(sP), 16, 1024);
+            // V read MN-major: 64 channels per 128-byte row, the next 64 one region further
+            const uint64_t v0 = ptx::sdesc_sw128(ptx::smem_u32(sV), kVRegion, 1024);
+            while (ok && walk.next(a, sg)) {
+                // (the first wait for the last segment's accumulators returns at once)
+                if (!ptx::mbar_wait(&S.o_free, sph, abort_flag)) break;
+                sph ^= 1;
+                for (int kt = sg.k0; ok && kt < sg.k1; ++kt) {
+                    if (!ptx::mbar_wait(&S.p_full, ph, abort_flag)) { ok = false; break; }
+                    ptx::tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (!ptx::mbar_wait(&S.v_full[i], ph, abort_flag)) { ok = false; break; }
+#pragma unroll
+                        for (int k = 0; k < kTile / 16; ++k)
+                            mma2_f16_ss(tmem + kOCol + 128 * i, p0 + (uint64_t)((k >> 2) * (8192 >> 4) + (k & 3) * 2),
+                                        v0 + (uint64_t)(i * (kVSlot >> 4) + k * (2048 >> 4)), idesc,
+                                        (kt > sg.k0 || k > 0) ? 1u : 0u);
+                        commit2(&S.v_empty[i]);
+                    }
+                    ph ^= 1;
+                }
+                if (ok) commit2(&S.seg_done);
+            }
+            commit2(&S.drain);
+            ptx::mbar_wait_drain(&S.drain, 0);
+        } else if (lane == 0) {
+            // ================= the second CTA's copies of V, passed on =================
+            while (ok && walk.next(a, sg))
+                for (int kt = sg.k0; ok && kt < sg.k1; ++kt, ph ^= 1)
+                    for (int i = 0; i < 2 && ok; ++i) {
+                        ok = ptx::mbar_wait(&S.v_full[i], ph, abort_flag);
+                        if (ok) arrive_first(&S.v_full[i]);
+                    }
+        }
+        __syncwarp();
+    } else if (warp >= kSoftWarp0) {
         // ================= softmax and partials =================
-        // The four warps of a quarter (16 queries, all keys) work together, apart from the others.
-        const int sub = warp & 3, quarter = (warp - 2) >> 2;
-        const int c0 = quarter * kCols;
-        const int wt = (threadIdx.x - 64) & 127;         // thread of the quarter
-        const uint32_t bar = 1 + quarter;
-        const int t = sub * 32 + lane;                   // key of the tile, and channel of a block
+        const int sub = warp & 3, hf = (warp - kSoftWarp0) >> 2;
+        const int tl = sub * 32 + lane;                  // TMEM lane
+        const int row = tl & 63, kh = tl >> 6;           // query; half of the keys (and of the channels)
         const uint32_t lane_addr = tmem + ((uint32_t)(sub * 32) << 16);
-        uint32_t ph = 0, sph = 0;
+        const uint32_t bar = 1 + (sub & 1);              // the four warps with the same queries
+        uint8_t *const p_row = sP + kh * 8192;
+        Ring<2> sb;
+        uint32_t pph = 1, sph = 0;                       // the last tile's second product; segments
         bool bad = false, aborted = false;
         while (!aborted && walk.next(a, sg)) {
-            const uint8_t *valid = a.valid + (int64_t)sg.g * a.n_pad + t;
-            if (wt < kCols) S.zm[c0 + wt] = make_float2(a.qs[sg.tile * kQ + c0 + wt], -INFINITY);
-            ptx::named_barrier(bar, 128);
-            float l[kCols];
-#pragma unroll
-            for (int i = 0; i < kCols; ++i) l[i] = 0.0f;
-            bool live_next = valid[(int64_t)sg.k0 * kTile] != 0;
+            const uint4 *valid = reinterpret_cast<const uint4 *>(a.valid + (int64_t)sg.g * a.n_pad + kh * 64 + hf * 32);
+            const float zs = a.qs[sg.tile * kQ + rank * kQHalf + row];
+            float mm = -INFINITY, l = 0.0f;              // running maximum - kShift; sum of the weights
+            uint4 va = valid[sg.k0 * (kTile / 16)], vb = valid[sg.k0 * (kTile / 16) + 1];
             for (int kt = sg.k0; kt < sg.k1; ++kt) {
-                const bool live = live_next;
-                if (kt + 1 < sg.k1) live_next = valid[(int64_t)(kt + 1) * kTile] != 0;
-                if (!ptx::mbar_wait(&S.s_full, ph, abort_flag)) bad = true;
-                ph ^= 1;
+                const uint32_t mask = key_mask(va, vb);
+                if (kt + 1 < sg.k1) {
+                    va = valid[(kt + 1) * (kTile / 16)];
+                    vb = valid[(kt + 1) * (kTile / 16) + 1];
+                }
+                if (!ptx::mbar_wait(&S.s_full[sb.st], sb.ph, abort_flag)) bad = true;
                 ptx::tc_fence_after();
-                uint32_t u[kCols];
-                ptx::tmem_ld16(lane_addr + c0, u);
+                uint32_t u[32];
+                ptx::tmem_ld32(lane_addr + sb.st * kSCols + hf * 32, u);
                 ptx::tmem_ld_wait();
-                // weights under the maxima so far, as the P^T line of this key; the first tile has none
-                // yet and goes on to the move below
-                float p[kCols];
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_first(&S.s_free[sb.st]);
+                sb.next();
+                float p[32];
                 auto weights = [&]() {
 #pragma unroll
-                    for (int c = 0; c < kCols / 8; ++c) {
-                        uint32_t w[4];
+                    for (int i = 0; i < 32; ++i) p[i] = ptx::ex2(fmaf(__uint_as_float(u[i]), zs, -mm));
+                    if (mask != 0xFFFFFFFFu) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int i = 8 * c + 2 * k;
-                            const float4 zm = *reinterpret_cast<const float4 *>(&S.zm[c0 + i]);
-                            p[i] = live ? ptx::ex2(fmaf(__uint_as_float(u[i]), zm.x, -zm.y)) : 0.0f;
-                            p[i + 1] = live ? ptx::ex2(fmaf(__uint_as_float(u[i + 1]), zm.z, -zm.w)) : 0.0f;
-                            const __half2 h = __floats2half2_rn(p[i], p[i + 1]);
-                            w[k] = *reinterpret_cast<const uint32_t *>(&h);
-                        }
-                        *reinterpret_cast<uint4 *>(sP + tc::sw128_off(t, quarter * 2 + c)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int i = 0; i < 32; ++i) p[i] = (mask >> i) & 1u ? p[i] : 0.0f;
                     }
                 };
+                // weights under the maximum so far; a segment's first tile has none yet
                 weights();
                 bool over = false;
 #pragma unroll
-                for (int i = 0; i < kCols; ++i) over |= p[i] > kOver;
+                for (int i = 0; i < 32; ++i) over |= p[i] > kOver;
+                float al = 1.0f;
                 // one barrier decides whether to stop and whether some maximum moves
                 if (tc::block_any(over || bad || *abort_flag != 0, bar, 128)) {
                     if (tc::block_any(bad || *abort_flag != 0, bar, 128)) { aborted = true; break; }
-                    float v[kCols];
+                    float top = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < kCols; ++i) v[i] = live ? __uint_as_float(u[i]) * S.zm[c0 + i].x : -INFINITY;
-                    reduce16<false>(v, lane);
-                    if (lane < kCols) S.red[sub][c0 + lane] = v[0];
+                    for (int i = 0; i < 32; ++i)
+                        if ((mask >> i) & 1u) top = fmaxf(top, __uint_as_float(u[i]) * zs);
+                    S.red[kh * 2 + hf][row] = top;
                     ptx::named_barrier(bar, 128);
-                    bool moved = false;
-                    if (wt < kCols) {
-                        const int c = c0 + wt;
-                        const float top = fmaxf(fmaxf(S.red[0][c], S.red[1][c]), fmaxf(S.red[2][c], S.red[3][c]));
-                        const float old = S.zm[c].y;     // maximum - kShift
-                        float al = 1.0f;
-                        if (top > old + (kShift + kLag)) {
-                            S.zm[c].y = top - kShift;
-                            al = old == -INFINITY ? 0.0f : ptx::ex2(old + kShift - top);
-                            moved = kt > sg.k0 && old != -INFINITY;
-                        }
-                        S.alpha[c] = al;
+                    top = fmaxf(fmaxf(S.red[0][row], S.red[1][row]), fmaxf(S.red[2][row], S.red[3][row]));
+                    if (top > mm + (kShift + kLag)) {
+                        al = mm == -INFINITY ? 0.0f : ptx::ex2(mm + kShift - top);
+                        mm = top - kShift;
+                        l *= al;
+                        weights();
                     }
-                    const bool rescale = tc::block_any(moved, bar, 128);
+                }
+                float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                uint32_t w[16];
 #pragma unroll
-                    for (int i = 0; i < kCols; ++i) l[i] *= S.alpha[c0 + i];
-                    weights();
-                    // accumulators of queries whose maximum moved: S(kt) completed after the last tile's
-                    // second product, so they are at rest
-                    if (rescale) {
+                for (int i = 0; i < 16; ++i) {
+                    add[i & 3] += p[2 * i] + p[2 * i + 1];
+                    const __half2 h = __floats2half2_rn(p[2 * i], p[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                l += (add[0] + add[1]) + (add[2] + add[3]);
+                // P and the accumulators are at rest once the last tile's second product is done
+                if (!ptx::mbar_wait(&S.v_empty[1], pph, abort_flag)) bad = true;
+                pph ^= 1;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<uint4 *>(p_row + tc::sw128_off(row, hf * 4 + q)) =
+                        make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+                // accumulators of queries whose maximum moved (al = 0: there is nothing in them yet)
+                if (__any_sync(0xffffffffu, kt > sg.k0 && al != 1.0f && al != 0.0f)) {
+                    ptx::tc_fence_after();
+                    const float f = al == 0.0f ? 1.0f : al;
 #pragma unroll 1
-                        for (int mb = 0; mb < kBlocks; ++mb) {
-                            uint32_t o[kCols];
-                            ptx::tmem_ld16(lane_addr + kOCol + kQ * mb + c0, o);
-                            ptx::tmem_ld_wait();
+                    for (int c = 0; c < 128; c += 32) {
+                        uint32_t o[32];
+                        ptx::tmem_ld32(lane_addr + kOCol + 128 * hf + c, o);
+                        ptx::tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < kCols; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * S.alpha[c0 + i]);
-                            ptx::tmem_st16(lane_addr + kOCol + kQ * mb + c0, o);
-                        }
-                        ptx::tmem_st_wait();
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        ptx::tmem_st32(lane_addr + kOCol + 128 * hf + c, o);
                     }
+                    ptx::tmem_st_wait();
                 }
                 ptx::fence_async_smem();
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&S.p_full);
-#pragma unroll
-                for (int i = 0; i < kCols; ++i) l[i] += p[i];
+                if (lane == 0) arrive_first(&S.p_full);
             }
             if (aborted) break;
             // ---- the segment's partial ----
@@ -542,35 +668,36 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap vmap, const
             sph ^= 1;
             if (tc::block_any(bad || *abort_flag != 0, bar, 128)) { aborted = true; break; }
             ptx::tc_fence_after();
-            float *part = a.parts + (blockIdx.x + sg.tile) * (int64_t)kPartFloats;
-            reduce16<true>(l, lane);
-            if (lane < kCols) S.red[sub][c0 + lane] = l[0];
+            float *part = a.parts + (2 * (pair + sg.tile) + rank) * (int64_t)kPartFloats;
+            S.red[kh * 2 + hf][row] = l;
             ptx::named_barrier(bar, 128);
-            if (wt < kCols) {
-                const int c = c0 + wt;
-                part[c] = S.zm[c].y;
-                part[kQ + c] = (S.red[0][c] + S.red[1][c]) + (S.red[2][c] + S.red[3][c]);
+            if (kh == 0 && hf == 0) {
+                part[row] = mm;
+                part[kQHalf + row] = (S.red[0][row] + S.red[1][row]) + (S.red[2][row] + S.red[3][row]);
             }
-#pragma unroll
-            for (int mb = 0; mb < kBlocks; ++mb) {
-                uint32_t o[kCols];
-                ptx::tmem_ld16(lane_addr + kOCol + kQ * mb + c0, o);
+            float *dst = part + 2 * kQHalf + row * kLatent + 256 * hf + 128 * kh;
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+                uint32_t o[32];
+                ptx::tmem_ld32(lane_addr + kOCol + 128 * hf + c, o);
                 ptx::tmem_ld_wait();
-                float *dst = part + 2 * kQ + c0 * kLatent + mb * 128 + t;
 #pragma unroll
-                for (int i = 0; i < kCols; ++i) dst[i * kLatent] = __uint_as_float(o[i]);
+                for (int q = 0; q < 8; ++q)
+                    *reinterpret_cast<uint4 *>(dst + c + 4 * q) = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
             }
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&S.o_free);
-            ptx::named_barrier(bar, 128);                // the shared maxima are read before they are reset
+            if (lane == 0) arrive_first(&S.o_free);
+            ptx::named_barrier(bar, 128);                // the sums are read before the next maxima are written
         }
     }
+    __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    cluster_sync();                                      // neither CTA's memory is in use any more
+    if (warp == 2) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, kTmemCols);
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)kTmemCols) : "memory");
     }
 }
 
@@ -583,13 +710,14 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const Args a) {
     const int g = find_group(a.groups, a.G, row, [](const Group &x) { return (int64_t)x.row0; });
     const Group gr = a.groups[g];
     int64_t c0 = 0, c1 = -1, tile = 0;
-    int qi = 0;
+    int side = 0, qi = 0;                                // the CTA of the pair, and its query
     const int64_t total = a.groups[a.G].work0;
     const int64_t nt = (gr.n + kTile - 1) / kTile;
     if (row >= gr.row0 && row < gr.row0 + gr.rows && nt > 0) {
         const int64_t i = f - (int64_t)gr.row0 * a.H;
         tile = gr.tile0 + i / kQ;
-        qi = (int)(i % kQ);
+        side = (int)(i % kQ) / kQHalf;
+        qi = (int)(i % kQHalf);
         // the shares that hold work items u0 .. u1 of this query tile; share c begins at total c / shares
         const int64_t shares = shares_of(a, total), u0 = gr.work0 + (i / kQ) * nt, u1 = u0 + nt - 1;
         c0 = u0 * shares / total;
@@ -601,17 +729,17 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const Args a) {
     const float own = a.own_lse ? a.own_lse[f] * kLog2e : -INFINITY;
     float top = own;
     for (int64_t c = c0; c <= c1; ++c) {
-        const float *p = a.parts + (c + tile) * (int64_t)kPartFloats;
-        if (p[kQ + qi] != 0.0f) top = fmaxf(top, p[qi]);
+        const float *p = a.parts + (2 * (c + tile) + side) * (int64_t)kPartFloats;
+        if (p[kQHalf + qi] != 0.0f) top = fmaxf(top, p[qi]);
     }
     float L = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int64_t c = c0; c <= c1; ++c) {
-        const float *p = a.parts + (c + tile) * (int64_t)kPartFloats;
-        const float ls = p[kQ + qi];
+        const float *p = a.parts + (2 * (c + tile) + side) * (int64_t)kPartFloats;
+        const float ls = p[kQHalf + qi];
         if (ls == 0.0f) continue;                        // no key of this piece counts
         const float w = exp2f(p[qi] - top);
         L += w * ls;
-        const float4 o = *reinterpret_cast<const float4 *>(p + 2 * kQ + qi * kLatent + threadIdx.x * 4);
+        const float4 o = *reinterpret_cast<const float4 *>(p + 2 * kQHalf + qi * kLatent + threadIdx.x * 4);
         acc[0] += w * o.x; acc[1] += w * o.y; acc[2] += w * o.z; acc[3] += w * o.w;
     }
     if (a.own_out && own != -INFINITY) {
@@ -639,7 +767,7 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const Args a) {
 // ---------------------------------------------------------------------------------------------
 struct Layout {
     int64_t n_pad, max_tiles;
-    int ctas;
+    int pairs;
     size_t groups, v, valid, qh, qs, parts, total;
 };
 inline Layout layout(int rows, int H, int G, int64_t max_n) {
@@ -647,7 +775,7 @@ inline Layout layout(int rows, int H, int G, int64_t max_n) {
     l.n_pad = ceil_div(max_n, (int64_t)kTile) * kTile;
     l.max_tiles = ceil_div((int64_t)rows * H, (int64_t)kQ) + G;
     const int64_t work = l.max_tiles * (l.n_pad / kTile);
-    l.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(device_sm_count(), work));
+    l.pairs = (int)std::max<int64_t>(1, std::min<int64_t>(device_sm_count() / 2, work));
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -659,7 +787,7 @@ inline Layout layout(int rows, int H, int G, int64_t max_n) {
     l.valid = take((size_t)G * l.n_pad);
     l.qh = take((size_t)l.max_tiles * kQ * kLatent * 2);
     l.qs = take((size_t)l.max_tiles * kQ * 4);
-    l.parts = take((size_t)(l.ctas + l.max_tiles) * kPartFloats * 4);
+    l.parts = take((size_t)(l.pairs + l.max_tiles) * 2 * kPartFloats * 4);
     l.total = off + 1024;
     return l;
 }
@@ -696,7 +824,7 @@ cudaError_t launch_prefix_attn(const uint16_t *q, int rows, int H, const int32_t
     a.qs = reinterpret_cast<float *>(ws + l.qs);
     a.parts = reinterpret_cast<float *>(ws + l.parts);
     a.max_tiles = l.max_tiles;
-    a.ctas = l.ctas;
+    a.pairs = l.pairs;
 
     const int prep_smem = (G + 1) * (int)sizeof(pfx::Group);
     e = ensure_smem_limit(g_prefix_prep_smem, pfx::prefix_prep_kernel, prep_smem);
@@ -708,7 +836,7 @@ cudaError_t launch_prefix_attn(const uint16_t *q, int rows, int H, const int32_t
     if (e != cudaSuccess) return e;
     int launches = 2;
     if (max_n > 0) {
-        CUtensorMap vmap, qmap;
+        CUtensorMap kmap, vmap, qmap;
         auto encode = [&](CUtensorMap *m, void *base, int64_t nrows, int box_rows) {
             const cuuint64_t dim[2] = {(cuuint64_t)kLatent, (cuuint64_t)nrows};
             const cuuint64_t strides[1] = {(cuuint64_t)kLatent * 2};
@@ -718,11 +846,12 @@ cudaError_t launch_prefix_attn(const uint16_t *q, int rows, int H, const int32_t
                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
         };
-        if (!encode(&vmap, a.v, (int64_t)G * l.n_pad, pfx::kTile) || !encode(&qmap, a.qh, l.max_tiles * pfx::kQ, pfx::kQ))
+        if (!encode(&kmap, a.v, (int64_t)G * l.n_pad, pfx::kKeyHalf) || !encode(&vmap, a.v, (int64_t)G * l.n_pad, pfx::kTile) ||
+            !encode(&qmap, a.qh, l.max_tiles * pfx::kQ, pfx::kQHalf))
             return cudaErrorInvalidValue;
         e = ensure_smem_limit(g_prefix_smem, pfx::prefix_attn_kernel, pfx::kSmemBytes);
         if (e != cudaSuccess) return e;
-        pfx::prefix_attn_kernel<<<(unsigned)l.ctas, pfx::kThreads, pfx::kSmemBytes, st>>>(a, vmap, qmap);
+        pfx::prefix_attn_kernel<<<(unsigned)(2 * l.pairs), pfx::kThreads, pfx::kSmemBytes, st>>>(a, kmap, vmap, qmap);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         launches = 3;
