@@ -9,10 +9,10 @@
 // the request's own entries and window), or nothing.
 //
 // Three launches:
-//  1. prefix_prep_kernel  every prefix entry once, to fp16 (E2M1 x E4M3 is exact in fp16), in a
-//     padded array of the workspace, through the block table; the queries to fp16, each row times
-//     a power of two that puts its largest element in [2^13, 2^14) (exact for all elements within
-//     2^27 of it, and a row of infinities or NaNs spoils no other); the groups' tile counts.
+//  1. prefix_prep_kernel  the cache row of every prefix entry, through the block table; the queries to
+//     fp16, each row times a power of two that puts its largest element in [2^13, 2^14) (exact for all
+//     elements within 2^27 of it, and a row of infinities or NaNs spoils no other); the groups' tile
+//     counts.
 //  2. prefix_attn_kernel  a persistent pair of CTAs per SM pair.  The work is the list of (128 queries,
 //     128 keys) tiles, all key tiles of one query tile after the other; pair i takes the i-th equal
 //     share, so every pair has the same number of tiles, and a query tile is cut at most where shares
@@ -31,21 +31,27 @@
 //                               the upper 128 channels; 2 x 128 columns)
 // With 64 queries per CTA the 512-wide accumulators take half of TMEM, which one CTA of 128 queries
 // could not hold next to S; both products read the latent from the two CTAs' shared memory, half
-// each.  S of the next tile runs under the softmax of this one: K and V come separately, in two halves
-// of the channels each, refilled as soon as their MMAs are done.
+// each.  S of the next tile runs under the softmax of this one: K and V are separate operands, in two
+// halves of the channels each, rewritten as soon as their MMAs are done.
+// The entries come as FP4 and are turned into fp16 (E2M1 x E4M3 is exact) on their way into shared
+// memory, by 8 warps that hold the next tile's codes in registers meanwhile: copies of fp16 entries
+// from a workspace took 128 KB of L2 reads per CTA and tile where the codes take 36, and the L2
+// delivered 6 TB/s of them at most (770 us for 128 rows x 64 heads on 32768 entries).
 // P is rounded to fp16 with the weights scaled to at most 2^15 (the maximum itself to 2^7), so weights
 // down to 2^-21 of the maximum keep 11 bits and the rest an absolute 2^-32: the rounding is at most
 // 2^-11 of sum_j p_j |v_j| / sum_j p_j plus n 2^-32 max |v|.
 //
-// Roles per CTA: warp 0 copies Q and K, warp 1 copies V; warps 2 and 3 issue the MMAs of S and of O
-// (first CTA) or pass the arrival of the second CTA's copies on to the first; warps 4-11 softmax and
-// partials.
+// Roles per CTA: warp 0 copies Q; warps 2 and 3 of the first CTA issue the MMAs of S and of O; warps
+// 4-11 softmax and partials; warps 12-15 entries to K, 16-19 to V.
 //
 // Bound: MMAs of N=128 take 46 cycles and N=256 60 (measured), 2432 a tile, and the tile's
-// shared-memory traffic (operands 224 KB, copies 128 KB, P 16 KB) 2900 cycles at 128 bytes a cycle.
+// shared-memory traffic (operands 224 KB, K and V 128 KB, P 16 KB) 2900 cycles at 128 bytes a cycle.
 // One CTA per 64 queries with S^T = V . Q^T (N=64, one 128 KB V buffer for both products, so that the
 // softmax lay between them) took 6400 cycles a tile: 825 us for 128 rows x 64 heads on 32768 entries.
 // Every wait is bounded: on expiry the CTA records CSA2_ERR_TIMEOUT, drains, frees TMEM and exits.
+#include <algorithm>
+#include <atomic>
+
 #include "common.cuh"
 #include "tc_ptx.cuh"
 
@@ -60,14 +66,16 @@ constexpr int kRegion = 64;                // channels of a 128-byte swizzled ro
 constexpr int kQRegion = kQHalf * 128;     // 8 KB
 constexpr int kKRegion = kKeyHalf * 128;   // 8 KB
 constexpr int kVRegion = kTile * 128;      // 16 KB
-constexpr int kKSlots = 2;                 // of 256 channels: 4 regions
+constexpr int kKHalves = 2;                // of 256 channels: 4 regions
 constexpr int kKSlot = 4 * kKRegion;
 constexpr int kVSlot = 2 * kVRegion;       // 128 channels, the CTA's half of an N=256 MMA
 constexpr int kQBytes = 8 * kQRegion;
 constexpr int kPBytes = kQHalf * kTile * 2;
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int kSoftWarp0 = 4;
 constexpr int kSoftWarps = 8;
+constexpr int kDeqWarp0 = 12;
+constexpr int kDeqWarps = 8;
 constexpr int kTmemCols = 512;
 constexpr int kSCols = 64;                 // a buffer of S; two from column 0
 constexpr int kOCol = 128;                 // two accumulators of 128 columns
@@ -103,8 +111,8 @@ struct Args {
     float *lse;
     // workspace
     Group *groups;                         // [G + 1]
-    __half *v;                             // [G][n_pad][512]
-    uint8_t *valid;                        // [G][n_pad]
+    int64_t *erow;                         // [G][n_pad]: cache rows of the entries, -1: none
+    uint8_t *valid;                        // [G][n_pad]: 1 where there is one
     __half *qh;                            // [tiles][128][512]
     float *qs;                             // [tiles][128]: logit per unit of S
     float *parts;                          // [pairs + tiles][2][kPartFloats]
@@ -113,7 +121,7 @@ struct Args {
 };
 
 // ---------------------------------------------------------------------------------------------
-// 1. entries and queries to fp16
+// 1. cache rows of the entries, queries to fp16
 // ---------------------------------------------------------------------------------------------
 constexpr int kPrepThreads = 256;
 
@@ -188,8 +196,9 @@ __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(const Args a)
     const int64_t nwarps = (int64_t)gridDim.x * (kPrepThreads / 32);
     const int64_t w0 = (int64_t)blockIdx.x * (kPrepThreads / 32) + warp;
 
-    // entries: a warp each, a lane per 16-channel block; rows up to the end of the last key tile
-    for (int64_t w = w0; w < (int64_t)a.G * a.n_pad; w += nwarps) {
+    // entries: a thread each, up to the end of the last key tile
+    const int64_t nthreads = (int64_t)gridDim.x * kPrepThreads;
+    for (int64_t w = (int64_t)blockIdx.x * kPrepThreads + threadIdx.x; w < (int64_t)a.G * a.n_pad; w += nthreads) {
         const int g = (int)(w / a.n_pad);
         const int64_t j = w - (int64_t)g * a.n_pad;
         const int n = gr[g].rows > 0 ? gr[g].n : 0;
@@ -205,27 +214,11 @@ __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(const Args a)
             }
             if (row < 0 || row >= a.kv_rows) {
                 row = -1;
-                if (lane == 0) raise_device_error(CSA2_ERR_INVALID_ARG);
+                raise_device_error(CSA2_ERR_INVALID_ARG);
             }
         }
-        uint4 o0 = make_uint4(0u, 0u, 0u, 0u), o1 = o0;
-        if (row >= 0) {
-            const uint8_t *p = a.kv + row * a.kv_row_stride;
-            const uint2 c = __ldg(reinterpret_cast<const uint2 *>(p) + lane);
-            const uint32_t s = ptx::e4m3x2_to_f16x2((uint16_t)__ldg(p + 256 + lane));
-            const uint32_t ss = __byte_perm(s, 0, 0x1010);
-            uint32_t h[4];
-            ptx::e2m1x8_to_f16x8(c.x, h);
-            o0 = make_uint4(ptx::hmul2_u32(h[0], ss), ptx::hmul2_u32(h[1], ss), ptx::hmul2_u32(h[2], ss),
-                            ptx::hmul2_u32(h[3], ss));
-            ptx::e2m1x8_to_f16x8(c.y, h);
-            o1 = make_uint4(ptx::hmul2_u32(h[0], ss), ptx::hmul2_u32(h[1], ss), ptx::hmul2_u32(h[2], ss),
-                            ptx::hmul2_u32(h[3], ss));
-        }
-        uint4 *dst = reinterpret_cast<uint4 *>(a.v + ((int64_t)g * a.n_pad + j) * kLatent) + lane * 2;
-        dst[0] = o0;
-        dst[1] = o1;
-        if (lane == 0) a.valid[(int64_t)g * a.n_pad + j] = row >= 0 ? 1 : 0;
+        a.erow[w] = row;
+        a.valid[w] = row >= 0 ? 1 : 0;
     }
 
     // queries: a warp each, 16 channels a lane; places past a group's last query are zero
@@ -265,13 +258,13 @@ __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(const Args a)
 // 2. tiles
 // ---------------------------------------------------------------------------------------------
 struct Ctl {
-    uint64_t k_full[kKSlots], k_empty[kKSlots], v_full[2], v_empty[2];
-    uint64_t q_full, q_empty, s_full[2], s_free[2], p_full, seg_done, o_free, drain;
+    uint64_t k_full[kKHalves], k_empty[kKHalves], v_full[2], v_empty[2];
+    uint64_t q_full, q_ready, q_empty, s_full[2], s_free[2], p_full, seg_done, o_free, drain;
     uint32_t tmem_base;
     int abort_flag;
     float red[4][kQHalf];
 };
-constexpr int kSmemBytes = kQBytes + kKSlots * kKSlot + 2 * kVSlot + kPBytes + (int)sizeof(Ctl) + 1024;
+constexpr int kSmemBytes = kQBytes + kKHalves * kKSlot + 2 * kVSlot + kPBytes + (int)sizeof(Ctl) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
 
 // A run of key tiles of one query tile: what a pair does between two changes of Q.
@@ -346,6 +339,48 @@ CSA2_D void cluster_sync() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// 128 channels of an entry: 64 bytes of codes and 8 scales.  No entry (row < 0): zeros.  The loads are
+// volatile so that they stay where they are issued, a tile ahead of their use.
+struct Piece {
+    uint4 c[4];
+    uint2 s;
+};
+CSA2_D void ldg16(const void *p, uint4 &v) {
+    asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+}
+CSA2_D void load_piece(const Args &a, int64_t row, int chan, Piece &x) {
+    if (row >= 0) {
+        const uint8_t *p = a.kv + row * a.kv_row_stride;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ldg16(p + chan / 2 + 16 * k, x.c[k]);
+        asm volatile("ld.global.nc.v2.b32 {%0,%1}, [%2];" : "=r"(x.s.x), "=r"(x.s.y) : "l"(p + 256 + chan / 16));
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x.c[k] = make_uint4(0u, 0u, 0u, 0u);
+        x.s = make_uint2(0u, 0u);
+    }
+}
+// Its fp16 values as row `row` of two swizzled regions `stride` bytes apart.
+CSA2_D void store_piece(uint8_t *region, int stride, int row, const Piece &x) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        const uint32_t w[8] = {x.c[2 * g].x, x.c[2 * g].y, x.c[2 * g].z, x.c[2 * g].w,
+                               x.c[2 * g + 1].x, x.c[2 * g + 1].y, x.c[2 * g + 1].z, x.c[2 * g + 1].w};
+        const uint32_t sw = g == 0 ? x.s.x : x.s.y;
+        const uint32_t s01 = ptx::e4m3x2_to_f16x2((uint16_t)(sw & 0xFFFFu)), s23 = ptx::e4m3x2_to_f16x2((uint16_t)(sw >> 16));
+        const uint32_t sc[4] = {__byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232), __byte_perm(s23, 0, 0x1010),
+                                __byte_perm(s23, 0, 0x3232)};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t h[4];
+            ptx::e2m1x8_to_f16x8(w[i], h);
+            const uint32_t f = sc[i >> 1];
+            *reinterpret_cast<uint4 *>(region + g * stride + tc::sw128_off(row, i)) =
+                make_uint4(ptx::hmul2_u32(h[0], f), ptx::hmul2_u32(h[1], f), ptx::hmul2_u32(h[2], f), ptx::hmul2_u32(h[3], f));
+        }
+    }
+}
+
 // Which of 32 keys count: their 32 bytes (0 or 1) as a bit mask.
 CSA2_D uint32_t key_mask(const uint4 &a, const uint4 &b) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -356,11 +391,10 @@ CSA2_D uint32_t key_mask(const uint4 &a, const uint4 &b) {
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                   const __grid_constant__ CUtensorMap qmap) {
+prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint8_t *sQ = base, *sK = sQ + kQBytes, *sV = sK + kKSlots * kKSlot, *sP = sV + 2 * kVSlot;
+    uint8_t *sQ = base, *sK = sQ + kQBytes, *sV = sK + kKHalves * kKSlot, *sP = sV + 2 * kVSlot;
     Ctl &S = *reinterpret_cast<Ctl *>(sP + kPBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)(blockIdx.x & 1), pair = (int)(blockIdx.x >> 1);
@@ -368,18 +402,17 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const
     if (walk.u >= walk.end) return;                      // both CTAs of the pair: nothing allocated yet
 
     if (threadIdx.x == 0) {
-        // the first CTA's "full" barriers also count the second CTA's copies
-        for (int i = 0; i < kKSlots; ++i) {
-            ptx::mbar_init(&S.k_full[i], rank == 0 ? 2 : 1);
-            ptx::mbar_init(&S.k_empty[i], 1);
-        }
+        // the first CTA's barriers for the MMAs count both CTAs' warps
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&S.v_full[i], rank == 0 ? 2 : 1);
+            ptx::mbar_init(&S.k_full[i], kDeqWarps);
+            ptx::mbar_init(&S.k_empty[i], 1);
+            ptx::mbar_init(&S.v_full[i], kDeqWarps);
             ptx::mbar_init(&S.v_empty[i], 1);
             ptx::mbar_init(&S.s_full[i], 1);
             ptx::mbar_init(&S.s_free[i], 2 * kSoftWarps);
         }
-        ptx::mbar_init(&S.q_full, rank == 0 ? 2 : 1);
+        ptx::mbar_init(&S.q_full, 1);
+        ptx::mbar_init(&S.q_ready, 2);
         ptx::mbar_init(&S.q_empty, 1);
         ptx::mbar_init(&S.p_full, 2 * kSoftWarps);
         ptx::mbar_init(&S.seg_done, 1);
@@ -403,74 +436,24 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const
     Segment sg;
 
     if (warp == 0) {
-        // ================= copies of Q and K =================
+        // ================= copies of Q =================
         if (lane == 0) {
-            Ring<kKSlots> kr;
-            uint32_t sph = 1;                            // parity of Q's last release
-            int used = 0, q_uses = 0;
-            bool ok = true;
-            while (ok && walk.next(a, sg)) {
-                const int32_t y0 = (int32_t)((int64_t)sg.g * a.n_pad) + rank * kKeyHalf;
-                for (int kt = sg.k0; ok && kt < sg.k1; ++kt) {
-                    for (int h = 0; h < kKSlots; ++h) {
-                        if (!ptx::mbar_wait(&S.k_empty[kr.st], kr.ph ^ 1, abort_flag)) { ok = false; break; }
-                        uint8_t *dst = sK + kr.st * kKSlot;
-                        ptx::mbar_arrive_expect_tx(&S.k_full[kr.st], kKSlot);
-                        for (int r = 0; r < 4; ++r)
-                            ptx::tma_load_2d(dst + r * kKRegion, &kmap, 256 * h + kRegion * r, y0 + kt * kTile, &S.k_full[kr.st]);
-                        kr.next();
-                        used = min(used + 1, kKSlots);
-                        if (kt == sg.k0 && h == 0) {     // Q once the last segment's scores are done
-                            if (!ptx::mbar_wait(&S.q_empty, sph, abort_flag)) { ok = false; break; }
-                            sph ^= 1;
-                            ptx::mbar_arrive_expect_tx(&S.q_full, kQBytes);
-                            for (int r = 0; r < 8; ++r)
-                                ptx::tma_load_2d(sQ + r * kQRegion, &qmap, r * kRegion,
-                                                 (int32_t)(sg.tile * kQ) + rank * kQHalf, &S.q_full);
-                            ++q_uses;
-                        }
-                    }
-                }
-            }
-            // copies in flight land before the CTA leaves (already so unless it gave up early)
-            for (; used > 0; --used) {
-                if (kr.st == 0) { kr.st = kKSlots; kr.ph ^= 1; }
-                --kr.st;
-                ptx::mbar_wait_drain(&S.k_full[kr.st], kr.ph);
-            }
-            if (q_uses > 0) ptx::mbar_wait_drain(&S.q_full, (q_uses - 1) & 1);
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ================= copies of V =================
-        if (lane == 0) {
-            Ring<2> vr;
-            int used = 0;
-            bool ok = true;
-            while (ok && walk.next(a, sg)) {
-                const int32_t y0 = (int32_t)((int64_t)sg.g * a.n_pad);
-                for (int kt = sg.k0; ok && kt < sg.k1; ++kt)
-                    for (int i = 0; i < 2; ++i) {
-                        if (!ptx::mbar_wait(&S.v_empty[vr.st], vr.ph ^ 1, abort_flag)) { ok = false; break; }
-                        uint8_t *dst = sV + vr.st * kVSlot;
-                        const int32_t x = 256 * i + 128 * rank;
-                        ptx::mbar_arrive_expect_tx(&S.v_full[vr.st], kVSlot);
-                        ptx::tma_load_2d(dst, &vmap, x, y0 + kt * kTile, &S.v_full[vr.st]);
-                        ptx::tma_load_2d(dst + kVRegion, &vmap, x + kRegion, y0 + kt * kTile, &S.v_full[vr.st]);
-                        vr.next();
-                        used = min(used + 1, 2);
-                    }
-            }
-            for (; used > 0; --used) {
-                if (vr.st == 0) { vr.st = 2; vr.ph ^= 1; }
-                --vr.st;
-                ptx::mbar_wait_drain(&S.v_full[vr.st], vr.ph);
+            uint32_t ph = 0;
+            while (walk.next(a, sg)) {
+                // once the last segment's scores are done (the first wait returns at once)
+                if (!ptx::mbar_wait(&S.q_empty, ph ^ 1, abort_flag)) break;
+                ptx::mbar_arrive_expect_tx(&S.q_full, kQBytes);
+                for (int r = 0; r < 8; ++r)
+                    ptx::tma_load_2d(sQ + r * kQRegion, &qmap, r * kRegion, (int32_t)(sg.tile * kQ) + rank * kQHalf, &S.q_full);
+                // (also so that no copy is in flight when the CTA leaves)
+                if (!ptx::mbar_wait_drain(&S.q_full, ph)) break;
+                arrive_first(&S.q_ready);
+                ph ^= 1;
             }
         }
         __syncwarp();
     } else if (warp == 2) {
-        Ring<kKSlots> kr;
-        uint32_t sph = 0;
+        uint32_t kph = 0, sph = 0;
         bool ok = true;
         if (lane == 0 && rank == 0) {
             // ================= scores: S = Q . V^T =================
@@ -479,15 +462,15 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const
             const uint64_t k0 = ptx::sdesc_sw128(ptx::smem_u32(sK), 16, 1024);
             Ring<2> sb;
             while (ok && walk.next(a, sg)) {
-                if (!ptx::mbar_wait(&S.q_full, sph, abort_flag)) break;
+                if (!ptx::mbar_wait(&S.q_ready, sph, abort_flag)) break;
                 sph ^= 1;
                 for (int kt = sg.k0; ok && kt < sg.k1; ++kt) {
                     // the softmax has read this buffer's last scores
                     if (!ptx::mbar_wait(&S.s_free[sb.st], sb.ph ^ 1, abort_flag)) { ok = false; break; }
                     ptx::tc_fence_after();
 #pragma unroll
-                    for (int h = 0; h < kKSlots; ++h) {
-                        if (!ptx::mbar_wait(&S.k_full[h], kr.ph, abort_flag)) { ok = false; break; }
+                    for (int h = 0; h < kKHalves; ++h) {
+                        if (!ptx::mbar_wait(&S.k_full[h], kph, abort_flag)) { ok = false; break; }
 #pragma unroll
                         for (int k = 0; k < 16; ++k)
                             mma2_f16_ss(tmem + sb.st * kSCols, q0 + (uint64_t)((4 * h + (k >> 2)) * (kQRegion >> 4) + (k & 3) * 2),
@@ -496,7 +479,7 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const
                         commit2(&S.k_empty[h]);
                     }
                     if (!ok) break;
-                    kr.ph ^= 1;
+                    kph ^= 1;
                     commit2(&S.s_full[sb.st]);
                     sb.next();
                 }
@@ -505,18 +488,6 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const
             // every issued MMA has completed before TMEM is released
             commit2(&S.drain);
             ptx::mbar_wait_drain(&S.drain, 0);
-        } else if (lane == 0) {
-            // ================= the second CTA's copies of Q and K, passed on =================
-            while (ok && walk.next(a, sg)) {
-                ok = ptx::mbar_wait(&S.q_full, sph, abort_flag);
-                sph ^= 1;
-                if (ok) arrive_first(&S.q_full);
-                for (int kt = sg.k0; ok && kt < sg.k1; ++kt)
-                    for (int h = 0; h < kKSlots && ok; ++h, kr.next()) {
-                        ok = ptx::mbar_wait(&S.k_full[kr.st], kr.ph, abort_flag);
-                        if (ok) arrive_first(&S.k_full[kr.st]);
-                    }
-            }
         }
         __syncwarp();
     } else if (warp == 3) {
@@ -553,17 +524,9 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const
             }
             commit2(&S.drain);
             ptx::mbar_wait_drain(&S.drain, 0);
-        } else if (lane == 0) {
-            // ================= the second CTA's copies of V, passed on =================
-            while (ok && walk.next(a, sg))
-                for (int kt = sg.k0; ok && kt < sg.k1; ++kt, ph ^= 1)
-                    for (int i = 0; i < 2 && ok; ++i) {
-                        ok = ptx::mbar_wait(&S.v_full[i], ph, abort_flag);
-                        if (ok) arrive_first(&S.v_full[i]);
-                    }
         }
         __syncwarp();
-    } else if (warp >= kSoftWarp0) {
+    } else if (warp >= kSoftWarp0 && warp < kDeqWarp0) {
         // ================= softmax and partials =================
         const int sub = warp & 3, hf = (warp - kSoftWarp0) >> 2;
         const int tl = sub * 32 + lane;                  // TMEM lane
@@ -587,15 +550,13 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const
                 }
                 if (!ptx::mbar_wait(&S.s_full[sb.st], sb.ph, abort_flag)) bad = true;
                 ptx::tc_fence_after();
-                uint32_t u[32];
-                ptx::tmem_ld32(lane_addr + sb.st * kSCols + hf * 32, u);
-                ptx::tmem_ld_wait();
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_first(&S.s_free[sb.st]);
-                sb.next();
+                // weights under the maximum so far; a segment's first tile has none yet
+                const uint32_t s_addr = lane_addr + sb.st * kSCols + hf * 32;
                 float p[32];
                 auto weights = [&]() {
+                    uint32_t u[32];
+                    ptx::tmem_ld32(s_addr, u);
+                    ptx::tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 32; ++i) p[i] = ptx::ex2(fmaf(__uint_as_float(u[i]), zs, -mm));
                     if (mask != 0xFFFFFFFFu) {
@@ -603,7 +564,6 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const
                         for (int i = 0; i < 32; ++i) p[i] = (mask >> i) & 1u ? p[i] : 0.0f;
                     }
                 };
-                // weights under the maximum so far; a segment's first tile has none yet
                 weights();
                 bool over = false;
 #pragma unroll
@@ -613,9 +573,14 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const
                 if (tc::block_any(over || bad || *abort_flag != 0, bar, 128)) {
                     if (tc::block_any(bad || *abort_flag != 0, bar, 128)) { aborted = true; break; }
                     float top = -INFINITY;
+                    {
+                        uint32_t u[32];
+                        ptx::tmem_ld32(s_addr, u);
+                        ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if ((mask >> i) & 1u) top = fmaxf(top, __uint_as_float(u[i]) * zs);
+                        for (int i = 0; i < 32; ++i)
+                            if ((mask >> i) & 1u) top = fmaxf(top, __uint_as_float(u[i]) * zs);
+                    }
                     S.red[kh * 2 + hf][row] = top;
                     ptx::named_barrier(bar, 128);
                     top = fmaxf(fmaxf(S.red[0][row], S.red[1][row]), fmaxf(S.red[2][row], S.red[3][row]));
@@ -623,9 +588,13 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const
                         al = mm == -INFINITY ? 0.0f : ptx::ex2(mm + kShift - top);
                         mm = top - kShift;
                         l *= al;
-                        weights();
                     }
+                    weights();
                 }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_first(&S.s_free[sb.st]);
+                sb.next();
                 float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 uint32_t w[16];
 #pragma unroll
@@ -689,6 +658,56 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const
             __syncwarp();
             if (lane == 0) arrive_first(&S.o_free);
             ptx::named_barrier(bar, 128);                // the sums are read before the next maxima are written
+        }
+    }
+    if (warp >= kDeqWarp0) {
+        // ================= entries to K (first four warps) and V (last four) =================
+        // A thread turns 128 channels of one entry into fp16 per half.  K: entry `key` of the CTA's 64,
+        // channels 256 h + 128 (lane / 16) ..; V: entry `key` of 128, the CTA's 128 channels of half h.
+        // Eight neighbouring lanes have neighbouring entries: their 16-byte stores meet no conflicts in
+        // the swizzled rows.
+        const int dw = (warp - kDeqWarp0) & 3;
+        const bool is_k = warp < kDeqWarp0 + 4;
+        const int key = is_k ? dw * 16 + (lane & 15) : dw * 32 + lane;
+        const int chan = is_k ? 128 * (lane >> 4) : 128 * rank;
+        const int off = is_k ? rank * kKeyHalf + key : key;                 // entry of the tile
+        const int stride = is_k ? kKRegion : kVRegion, slot = is_k ? kKSlot : kVSlot;
+        uint8_t *const dst = is_k ? sK + (lane >> 4) * 2 * kKRegion : sV;
+        uint64_t *const full = is_k ? S.k_full : S.v_full, *const empty = is_k ? S.k_empty : S.v_empty;
+        bool more = walk.next(a, sg);
+        int kt = sg.k0;
+        // the cache row of this thread's entry in the next tile of the walk; -2 behind the last tile
+        auto next_row = [&]() -> int64_t {
+            if (!more) return -2;
+            const int64_t r = a.erow[(int64_t)sg.g * a.n_pad + (int64_t)kt * kTile + off];
+            if (++kt >= sg.k1) {
+                more = walk.next(a, sg);
+                kt = sg.k0;
+            }
+            return r;
+        };
+        uint32_t ph = 1;                                 // the operand's last release
+        Piece x[2];
+        int64_t row = next_row();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) load_piece(a, row, 256 * h + chan, x[h]);
+        int64_t row1 = next_row();
+        while (row != -2) {
+            const int64_t row2 = next_row();             // two tiles ahead: its load is over when it is used
+            bool bad = false;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (!ptx::mbar_wait(&empty[h], ph, abort_flag)) bad = true;
+                store_piece(dst + h * slot, stride, key, x[h]);
+                ptx::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive_first(&full[h]);
+                load_piece(a, row1, 256 * h + chan, x[h]);
+            }
+            if (__any_sync(0xffffffffu, bad)) break;
+            ph ^= 1;
+            row = row1;
+            row1 = row2;
         }
     }
     __syncwarp();
@@ -765,17 +784,47 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const Args a) {
 // ---------------------------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------------------------
+// CTA pairs that can be resident at once (a GPC with an odd number of SMs leaves one out): a pair
+// more than that would run after all others.  Asked once per device; 74 where none is visible.
+inline int resident_pairs() {
+    static std::atomic<int> cache[kMaxDevices];
+    const int dev = current_device();
+    if (dev < 0) return 74;
+    int n = cache[dev].load(std::memory_order_acquire);
+    if (n > 0) return n;
+    static SmemLimit lim;
+    if (ensure_smem_limit(lim, prefix_attn_kernel, kSmemBytes) == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * 512);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmemBytes;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 2;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, prefix_attn_kernel, &cfg) != cudaSuccess) n = 0;
+    }
+    if (n <= 0) {
+        cudaGetLastError();                              // an answer is not needed: fewer pairs are only slower
+        n = std::max(1, device_sm_count() / 2);
+    }
+    cache[dev].store(n, std::memory_order_release);
+    return n;
+}
+
 struct Layout {
     int64_t n_pad, max_tiles;
     int pairs;
-    size_t groups, v, valid, qh, qs, parts, total;
+    size_t groups, erow, valid, qh, qs, parts, total;
 };
 inline Layout layout(int rows, int H, int G, int64_t max_n) {
     Layout l;
     l.n_pad = ceil_div(max_n, (int64_t)kTile) * kTile;
     l.max_tiles = ceil_div((int64_t)rows * H, (int64_t)kQ) + G;
     const int64_t work = l.max_tiles * (l.n_pad / kTile);
-    l.pairs = (int)std::max<int64_t>(1, std::min<int64_t>(device_sm_count() / 2, work));
+    l.pairs = (int)std::max<int64_t>(1, std::min<int64_t>(resident_pairs(), work));
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -783,7 +832,7 @@ inline Layout layout(int rows, int H, int G, int64_t max_n) {
         return at;
     };
     l.groups = take((size_t)(G + 1) * sizeof(Group));
-    l.v = take((size_t)G * l.n_pad * kLatent * 2);
+    l.erow = take((size_t)G * l.n_pad * 8);
     l.valid = take((size_t)G * l.n_pad);
     l.qh = take((size_t)l.max_tiles * kQ * kLatent * 2);
     l.qs = take((size_t)l.max_tiles * kQ * 4);
@@ -818,7 +867,7 @@ cudaError_t launch_prefix_attn(const uint16_t *q, int rows, int H, const int32_t
     a.own_out = own_out; a.own_lse = own_lse;
     a.out = out; a.out_dtype = out_dtype; a.lse = lse;
     a.groups = reinterpret_cast<pfx::Group *>(ws + l.groups);
-    a.v = reinterpret_cast<__half *>(ws + l.v);
+    a.erow = reinterpret_cast<int64_t *>(ws + l.erow);
     a.valid = ws + l.valid;
     a.qh = reinterpret_cast<__half *>(ws + l.qh);
     a.qs = reinterpret_cast<float *>(ws + l.qs);
@@ -829,14 +878,14 @@ cudaError_t launch_prefix_attn(const uint16_t *q, int rows, int H, const int32_t
     const int prep_smem = (G + 1) * (int)sizeof(pfx::Group);
     e = ensure_smem_limit(g_prefix_prep_smem, pfx::prefix_prep_kernel, prep_smem);
     if (e != cudaSuccess) return e;
-    const int64_t warps = std::max<int64_t>((int64_t)G * l.n_pad, l.max_tiles * pfx::kQ);
+    const int64_t warps = std::max<int64_t>(ceil_div((int64_t)G * l.n_pad, (int64_t)32), l.max_tiles * pfx::kQ);
     const int64_t blocks = std::min<int64_t>(ceil_div(warps, (int64_t)(pfx::kPrepThreads / 32)), (int64_t)device_sm_count() * 8);
     pfx::prefix_prep_kernel<<<(unsigned)blocks, pfx::kPrepThreads, prep_smem, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     int launches = 2;
     if (max_n > 0) {
-        CUtensorMap kmap, vmap, qmap;
+        CUtensorMap qmap;
         auto encode = [&](CUtensorMap *m, void *base, int64_t nrows, int box_rows) {
             const cuuint64_t dim[2] = {(cuuint64_t)kLatent, (cuuint64_t)nrows};
             const cuuint64_t strides[1] = {(cuuint64_t)kLatent * 2};
@@ -846,12 +895,11 @@ cudaError_t launch_prefix_attn(const uint16_t *q, int rows, int H, const int32_t
                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
         };
-        if (!encode(&kmap, a.v, (int64_t)G * l.n_pad, pfx::kKeyHalf) || !encode(&vmap, a.v, (int64_t)G * l.n_pad, pfx::kTile) ||
-            !encode(&qmap, a.qh, l.max_tiles * pfx::kQ, pfx::kQHalf))
+        if (!encode(&qmap, a.qh, l.max_tiles * pfx::kQ, pfx::kQHalf))
             return cudaErrorInvalidValue;
         e = ensure_smem_limit(g_prefix_smem, pfx::prefix_attn_kernel, pfx::kSmemBytes);
         if (e != cudaSuccess) return e;
-        pfx::prefix_attn_kernel<<<(unsigned)(2 * l.pairs), pfx::kThreads, pfx::kSmemBytes, st>>>(a, kmap, vmap, qmap);
+        pfx::prefix_attn_kernel<<<(unsigned)(2 * l.pairs), pfx::kThreads, pfx::kSmemBytes, st>>>(a, qmap);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         launches = 3;
