@@ -42,7 +42,8 @@
 // 2^-11 of sum_j p_j |v_j| / sum_j p_j plus n 2^-32 max |v|.
 //
 // Roles per CTA: warp 0 copies Q; warps 2 and 3 of the first CTA issue the MMAs of S and of O; warps
-// 4-11 softmax and partials; warps 12-15 entries to K, 16-19 to V.
+// 4-11 softmax and partials; warps 12-19 entries to K, 20-27 to V (half as many, with twice the
+// channels each: 692 us; their chain of wait, conversion, store and arrival was the longest).
 //
 // Bound: MMAs of N=128 take 46 cycles and N=256 60 (measured), 2432 a tile, and the tile's
 // shared-memory traffic (operands 224 KB, K and V 128 KB, P 16 KB) 2900 cycles at 128 bytes a cycle.
@@ -71,11 +72,17 @@ constexpr int kKSlot = 4 * kKRegion;
 constexpr int kVSlot = 2 * kVRegion;       // 128 channels, the CTA's half of an N=256 MMA
 constexpr int kQBytes = 8 * kQRegion;
 constexpr int kPBytes = kQHalf * kTile * 2;
-constexpr int kThreads = 640;
+constexpr int kThreads = 896;
 constexpr int kSoftWarp0 = 4;
 constexpr int kSoftWarps = 8;
 constexpr int kDeqWarp0 = 12;
-constexpr int kDeqWarps = 8;
+constexpr int kDeqWarps = 8;              // for K, and as many for V
+// Registers per thread of the first four warps, the softmax's and the entries': the launch's 72 x 896,
+// dealt out again.
+constexpr int kRegsLaunch = 72, kRegsIssue = 56, kRegsSoft = 96, kRegsDeq = 64;
+static_assert(128 * kRegsIssue + 32 * kSoftWarps * kRegsSoft + 64 * kDeqWarps * kRegsDeq <= kThreads * kRegsLaunch &&
+                  kThreads * kRegsLaunch <= 65536,
+              "a warp group that waited for more registers than there are would wait forever");
 constexpr int kTmemCols = 512;
 constexpr int kSCols = 64;                 // a buffer of S; two from column 0
 constexpr int kOCol = 128;                 // two accumulators of 128 columns
@@ -189,6 +196,7 @@ __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(const Args a)
     extern __shared__ __align__(16) uint8_t smem[];
     Group *gr = reinterpret_cast<Group *>(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 0) scan_groups(a, gr, lane, blockIdx.x == 0);
     __syncthreads();
     if (blockIdx.x == 0)
@@ -339,45 +347,38 @@ CSA2_D void cluster_sync() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// 128 channels of an entry: 64 bytes of codes and 8 scales.  No entry (row < 0): zeros.  The loads are
+// 64 channels of an entry: 32 bytes of codes and 4 scales.  No entry (row < 0): zeros.  The loads are
 // volatile so that they stay where they are issued, a tile ahead of their use.
 struct Piece {
-    uint4 c[4];
-    uint2 s;
+    uint4 c[2];
+    uint32_t s;
 };
-CSA2_D void ldg16(const void *p, uint4 &v) {
-    asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-}
 CSA2_D void load_piece(const Args &a, int64_t row, int chan, Piece &x) {
     if (row >= 0) {
         const uint8_t *p = a.kv + row * a.kv_row_stride;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) ldg16(p + chan / 2 + 16 * k, x.c[k]);
-        asm volatile("ld.global.nc.v2.b32 {%0,%1}, [%2];" : "=r"(x.s.x), "=r"(x.s.y) : "l"(p + 256 + chan / 16));
+        for (int k = 0; k < 2; ++k)
+            asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(x.c[k].x), "=r"(x.c[k].y), "=r"(x.c[k].z), "=r"(x.c[k].w) : "l"(p + chan / 2 + 16 * k));
+        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(x.s) : "l"(p + 256 + chan / 16));
     } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x.c[k] = make_uint4(0u, 0u, 0u, 0u);
-        x.s = make_uint2(0u, 0u);
+        x.c[0] = x.c[1] = make_uint4(0u, 0u, 0u, 0u);
+        x.s = 0u;
     }
 }
-// Its fp16 values as row `row` of two swizzled regions `stride` bytes apart.
-CSA2_D void store_piece(uint8_t *region, int stride, int row, const Piece &x) {
+// Its fp16 values as row `row` of a swizzled region.
+CSA2_D void store_piece(uint8_t *region, int row, const Piece &x) {
+    const uint32_t w[8] = {x.c[0].x, x.c[0].y, x.c[0].z, x.c[0].w, x.c[1].x, x.c[1].y, x.c[1].z, x.c[1].w};
+    const uint32_t s01 = ptx::e4m3x2_to_f16x2((uint16_t)(x.s & 0xFFFFu)), s23 = ptx::e4m3x2_to_f16x2((uint16_t)(x.s >> 16));
+    const uint32_t sc[4] = {__byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232), __byte_perm(s23, 0, 0x1010),
+                            __byte_perm(s23, 0, 0x3232)};
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        const uint32_t w[8] = {x.c[2 * g].x, x.c[2 * g].y, x.c[2 * g].z, x.c[2 * g].w,
-                               x.c[2 * g + 1].x, x.c[2 * g + 1].y, x.c[2 * g + 1].z, x.c[2 * g + 1].w};
-        const uint32_t sw = g == 0 ? x.s.x : x.s.y;
-        const uint32_t s01 = ptx::e4m3x2_to_f16x2((uint16_t)(sw & 0xFFFFu)), s23 = ptx::e4m3x2_to_f16x2((uint16_t)(sw >> 16));
-        const uint32_t sc[4] = {__byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232), __byte_perm(s23, 0, 0x1010),
-                                __byte_perm(s23, 0, 0x3232)};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t h[4];
-            ptx::e2m1x8_to_f16x8(w[i], h);
-            const uint32_t f = sc[i >> 1];
-            *reinterpret_cast<uint4 *>(region + g * stride + tc::sw128_off(row, i)) =
-                make_uint4(ptx::hmul2_u32(h[0], f), ptx::hmul2_u32(h[1], f), ptx::hmul2_u32(h[2], f), ptx::hmul2_u32(h[3], f));
-        }
+    for (int i = 0; i < 8; ++i) {
+        uint32_t h[4];
+        ptx::e2m1x8_to_f16x8(w[i], h);
+        const uint32_t f = sc[i >> 1];
+        *reinterpret_cast<uint4 *>(region + tc::sw128_off(row, i)) =
+            make_uint4(ptx::hmul2_u32(h[0], f), ptx::hmul2_u32(h[1], f), ptx::hmul2_u32(h[2], f), ptx::hmul2_u32(h[3], f));
     }
 }
 
@@ -398,15 +399,12 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
     Ctl &S = *reinterpret_cast<Ctl *>(sP + kPBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)(blockIdx.x & 1), pair = (int)(blockIdx.x >> 1);
-    Walk walk = walk_of(a, pair);
-    if (walk.u >= walk.end) return;                      // both CTAs of the pair: nothing allocated yet
-
     if (threadIdx.x == 0) {
         // the first CTA's barriers for the MMAs count both CTAs' warps
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&S.k_full[i], kDeqWarps);
+            ptx::mbar_init(&S.k_full[i], 2 * kDeqWarps);
             ptx::mbar_init(&S.k_empty[i], 1);
-            ptx::mbar_init(&S.v_full[i], kDeqWarps);
+            ptx::mbar_init(&S.v_full[i], 2 * kDeqWarps);
             ptx::mbar_init(&S.v_empty[i], 1);
             ptx::mbar_init(&S.s_full[i], 1);
             ptx::mbar_init(&S.s_free[i], 2 * kSoftWarps);
@@ -433,101 +431,109 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
     ptx::tc_fence_after();
     const uint32_t tmem = S.tmem_base;
     volatile int *abort_flag = &S.abort_flag;
+    // everything above runs beside the first launch; its results are there from here on
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    Walk walk = walk_of(a, pair);                        // (may be empty: every role's loop then is)
     Segment sg;
 
-    if (warp == 0) {
-        // ================= copies of Q =================
-        if (lane == 0) {
-            uint32_t ph = 0;
-            while (walk.next(a, sg)) {
-                // once the last segment's scores are done (the first wait returns at once)
-                if (!ptx::mbar_wait(&S.q_empty, ph ^ 1, abort_flag)) break;
-                ptx::mbar_arrive_expect_tx(&S.q_full, kQBytes);
-                for (int r = 0; r < 8; ++r)
-                    ptx::tma_load_2d(sQ + r * kQRegion, &qmap, r * kRegion, (int32_t)(sg.tile * kQ) + rank * kQHalf, &S.q_full);
-                // (also so that no copy is in flight when the CTA leaves)
-                if (!ptx::mbar_wait_drain(&S.q_full, ph)) break;
-                arrive_first(&S.q_ready);
-                ph ^= 1;
-            }
-        }
-        __syncwarp();
-    } else if (warp == 2) {
-        uint32_t kph = 0, sph = 0;
-        bool ok = true;
-        if (lane == 0 && rank == 0) {
-            // ================= scores: S = Q . V^T =================
-            constexpr uint32_t idesc = ptx::idesc_f16_f32(128, kTile, false, false);
-            const uint64_t q0 = ptx::sdesc_sw128(ptx::smem_u32(sQ), 16, 1024);
-            const uint64_t k0 = ptx::sdesc_sw128(ptx::smem_u32(sK), 16, 1024);
-            Ring<2> sb;
-            while (ok && walk.next(a, sg)) {
-                if (!ptx::mbar_wait(&S.q_ready, sph, abort_flag)) break;
-                sph ^= 1;
-                for (int kt = sg.k0; ok && kt < sg.k1; ++kt) {
-                    // the softmax has read this buffer's last scores
-                    if (!ptx::mbar_wait(&S.s_free[sb.st], sb.ph ^ 1, abort_flag)) { ok = false; break; }
-                    ptx::tc_fence_after();
-#pragma unroll
-                    for (int h = 0; h < kKHalves; ++h) {
-                        if (!ptx::mbar_wait(&S.k_full[h], kph, abort_flag)) { ok = false; break; }
-#pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            mma2_f16_ss(tmem + sb.st * kSCols, q0 + (uint64_t)((4 * h + (k >> 2)) * (kQRegion >> 4) + (k & 3) * 2),
-                                        k0 + (uint64_t)(h * (kKSlot >> 4) + (k >> 2) * (kKRegion >> 4) + (k & 3) * 2), idesc,
-                                        (h | k) != 0);
-                        commit2(&S.k_empty[h]);
-                    }
-                    if (!ok) break;
-                    kph ^= 1;
-                    commit2(&S.s_full[sb.st]);
-                    sb.next();
-                }
-                if (ok) commit2(&S.q_empty);
-            }
-            // every issued MMA has completed before TMEM is released
-            commit2(&S.drain);
-            ptx::mbar_wait_drain(&S.drain, 0);
-        }
-        __syncwarp();
-    } else if (warp == 3) {
-        uint32_t ph = 0, sph = 1;                        // tiles; the last segment's accumulators
-        bool ok = true;
-        if (lane == 0 && rank == 0) {
-            // ================= output: O += P . V =================
-            // A thread of its own: its waits and commits (150 and 60 cycles each, during which a thread's
-            // MMAs stand still) run under the scores' MMAs, and the other way round.
-            constexpr uint32_t idesc = ptx::idesc_f16_f32(128, 256, false, true);
-            const uint64_t p0 = ptx::sdesc_sw128(ptx::smem_u32(sP), 16, 1024);
-            // V read MN-major: 64 channels per 128-byte row, the next 64 one region further
-            const uint64_t v0 = ptx::sdesc_sw128(ptx::smem_u32(sV), kVRegion, 1024);
-            while (ok && walk.next(a, sg)) {
-                // (the first wait for the last segment's accumulators returns at once)
-                if (!ptx::mbar_wait(&S.o_free, sph, abort_flag)) break;
-                sph ^= 1;
-                for (int kt = sg.k0; ok && kt < sg.k1; ++kt) {
-                    if (!ptx::mbar_wait(&S.p_full, ph, abort_flag)) { ok = false; break; }
-                    ptx::tc_fence_after();
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (!ptx::mbar_wait(&S.v_full[i], ph, abort_flag)) { ok = false; break; }
-#pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k)
-                            mma2_f16_ss(tmem + kOCol + 128 * i, p0 + (uint64_t)((k >> 2) * (8192 >> 4) + (k & 3) * 2),
-                                        v0 + (uint64_t)(i * (kVSlot >> 4) + k * (2048 >> 4)), idesc,
-                                        (kt > sg.k0 || k > 0) ? 1u : 0u);
-                        commit2(&S.v_empty[i]);
-                    }
+    if (warp < kSoftWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+        if (warp == 0) {
+            // ================= copies of Q =================
+            if (lane == 0) {
+                uint32_t ph = 0;
+                while (walk.next(a, sg)) {
+                    // once the last segment's scores are done (the first wait returns at once)
+                    if (!ptx::mbar_wait(&S.q_empty, ph ^ 1, abort_flag)) break;
+                    ptx::mbar_arrive_expect_tx(&S.q_full, kQBytes);
+                    for (int r = 0; r < 8; ++r)
+                        ptx::tma_load_2d(sQ + r * kQRegion, &qmap, r * kRegion, (int32_t)(sg.tile * kQ) + rank * kQHalf, &S.q_full);
+                    // (also so that no copy is in flight when the CTA leaves)
+                    if (!ptx::mbar_wait_drain(&S.q_full, ph)) break;
+                    arrive_first(&S.q_ready);
                     ph ^= 1;
                 }
-                if (ok) commit2(&S.seg_done);
             }
-            commit2(&S.drain);
-            ptx::mbar_wait_drain(&S.drain, 0);
+            __syncwarp();
+        } else if (warp == 2) {
+            uint32_t kph = 0, sph = 0;
+            bool ok = true;
+            if (lane == 0 && rank == 0) {
+                // ================= scores: S = Q . V^T =================
+                constexpr uint32_t idesc = ptx::idesc_f16_f32(128, kTile, false, false);
+                const uint64_t q0 = ptx::sdesc_sw128(ptx::smem_u32(sQ), 16, 1024);
+                const uint64_t k0 = ptx::sdesc_sw128(ptx::smem_u32(sK), 16, 1024);
+                Ring<2> sb;
+                while (ok && walk.next(a, sg)) {
+                    if (!ptx::mbar_wait(&S.q_ready, sph, abort_flag)) break;
+                    sph ^= 1;
+                    for (int kt = sg.k0; ok && kt < sg.k1; ++kt) {
+                        // the softmax has read this buffer's last scores
+                        if (!ptx::mbar_wait(&S.s_free[sb.st], sb.ph ^ 1, abort_flag)) { ok = false; break; }
+                        ptx::tc_fence_after();
+#pragma unroll
+                        for (int h = 0; h < kKHalves; ++h) {
+                            if (!ptx::mbar_wait(&S.k_full[h], kph, abort_flag)) { ok = false; break; }
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                mma2_f16_ss(tmem + sb.st * kSCols, q0 + (uint64_t)((4 * h + (k >> 2)) * (kQRegion >> 4) + (k & 3) * 2),
+                                            k0 + (uint64_t)(h * (kKSlot >> 4) + (k >> 2) * (kKRegion >> 4) + (k & 3) * 2), idesc,
+                                            (h | k) != 0);
+                            commit2(&S.k_empty[h]);
+                        }
+                        if (!ok) break;
+                        kph ^= 1;
+                        commit2(&S.s_full[sb.st]);
+                        sb.next();
+                    }
+                    if (ok) commit2(&S.q_empty);
+                }
+                // every issued MMA has completed before TMEM is released
+                commit2(&S.drain);
+                ptx::mbar_wait_drain(&S.drain, 0);
+            }
+            __syncwarp();
+        } else if (warp == 3) {
+            uint32_t ph = 0, sph = 1;                        // tiles; the last segment's accumulators
+            bool ok = true;
+            if (lane == 0 && rank == 0) {
+                // ================= output: O += P . V =================
+                // A thread of its own: its waits and commits (150 and 60 cycles each, during which a thread's
+                // MMAs stand still) run under the scores' MMAs, and the other way round.
+                constexpr uint32_t idesc = ptx::idesc_f16_f32(128, 256, false, true);
+                const uint64_t p0 = ptx::sdesc_sw128(ptx::smem_u32(sP), 16, 1024);
+                // V read MN-major: 64 channels per 128-byte row, the next 64 one region further
+                const uint64_t v0 = ptx::sdesc_sw128(ptx::smem_u32(sV), kVRegion, 1024);
+                while (ok && walk.next(a, sg)) {
+                    // (the first wait for the last segment's accumulators returns at once)
+                    if (!ptx::mbar_wait(&S.o_free, sph, abort_flag)) break;
+                    sph ^= 1;
+                    for (int kt = sg.k0; ok && kt < sg.k1; ++kt) {
+                        if (!ptx::mbar_wait(&S.p_full, ph, abort_flag)) { ok = false; break; }
+                        ptx::tc_fence_after();
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (!ptx::mbar_wait(&S.v_full[i], ph, abort_flag)) { ok = false; break; }
+#pragma unroll
+                            for (int k = 0; k < kTile / 16; ++k)
+                                mma2_f16_ss(tmem + kOCol + 128 * i, p0 + (uint64_t)((k >> 2) * (8192 >> 4) + (k & 3) * 2),
+                                            v0 + (uint64_t)(i * (kVSlot >> 4) + k * (2048 >> 4)), idesc,
+                                            (kt > sg.k0 || k > 0) ? 1u : 0u);
+                            commit2(&S.v_empty[i]);
+                        }
+                        ph ^= 1;
+                    }
+                    if (ok) commit2(&S.seg_done);
+                }
+                commit2(&S.drain);
+                ptx::mbar_wait_drain(&S.drain, 0);
+            }
+            __syncwarp();
         }
-        __syncwarp();
-    } else if (warp >= kSoftWarp0 && warp < kDeqWarp0) {
+    } else if (warp < kDeqWarp0) {
         // ================= softmax and partials =================
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
         const int sub = warp & 3, hf = (warp - kSoftWarp0) >> 2;
         const int tl = sub * 32 + lane;                  // TMEM lane
         const int row = tl & 63, kh = tl >> 6;           // query; half of the keys (and of the channels)
@@ -644,15 +650,27 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
                 part[row] = mm;
                 part[kQHalf + row] = (S.red[0][row] + S.red[1][row]) + (S.red[2][row] + S.red[3][row]);
             }
-            float *dst = part + 2 * kQHalf + row * kLatent + 256 * hf + 128 * kh;
+            // 16 columns at a time through this warp's own bytes of P (at rest now), so that four lanes
+            // store 64 bytes of a row together
+            float *dst = part + 2 * kQHalf + 256 * hf + 128 * kh + 4 * (lane & 3);
+            const int r0 = (sub & 1) * 32;               // the warp's first query
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-                uint32_t o[32];
-                ptx::tmem_ld32(lane_addr + kOCol + 128 * hf + c, o);
+            for (int c = 0; c < 128; c += 16) {
+                uint32_t o[16];
+                ptx::tmem_ld16(lane_addr + kOCol + 128 * hf + c, o);
                 ptx::tmem_ld_wait();
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    *reinterpret_cast<uint4 *>(dst + c + 4 * q) = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<uint4 *>(p_row + tc::sw128_off(row, hf * 4 + q)) =
+                        make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = r0 + 8 * k + (lane >> 2);
+                    *reinterpret_cast<uint4 *>(dst + r * kLatent + c) =
+                        *reinterpret_cast<const uint4 *>(p_row + tc::sw128_off(r, hf * 4 + (lane & 3)));
+                }
+                __syncwarp();
             }
             ptx::tc_fence_before();
             __syncwarp();
@@ -660,22 +678,23 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
             ptx::named_barrier(bar, 128);                // the sums are read before the next maxima are written
         }
     }
-    if (warp >= kDeqWarp0) {
-        // ================= entries to K (first four warps) and V (last four) =================
-        // A thread turns 128 channels of one entry into fp16 per half.  K: entry `key` of the CTA's 64,
-        // channels 256 h + 128 (lane / 16) ..; V: entry `key` of 128, the CTA's 128 channels of half h.
-        // Eight neighbouring lanes have neighbouring entries: their 16-byte stores meet no conflicts in
-        // the swizzled rows.
-        const int dw = (warp - kDeqWarp0) & 3;
-        const bool is_k = warp < kDeqWarp0 + 4;
-        const int key = is_k ? dw * 16 + (lane & 15) : dw * 32 + lane;
-        const int chan = is_k ? 128 * (lane >> 4) : 128 * rank;
+    else {
+        // ================= entries to K (first eight warps) and V (last eight) =================
+        // A thread turns 64 channels of one entry into fp16 per half.  K: entry `key` of the CTA's 64,
+        // channels 256 h + 64 (lane / 8) ..; V: entry `key` of 128, channels 64 (lane / 16) .. of the CTA's
+        // 128 of half h.  Eight neighbouring lanes have neighbouring entries: their 16-byte stores meet
+        // no conflicts in the swizzled rows.
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDeq));
+        const bool is_k = warp < kDeqWarp0 + kDeqWarps;
+        const int dw = (warp - kDeqWarp0) & (kDeqWarps - 1);
+        const int key = is_k ? dw * 8 + (lane & 7) : dw * 16 + (lane & 15);
+        const int chan = is_k ? 64 * (lane >> 3) : 128 * rank + 64 * (lane >> 4);
         const int off = is_k ? rank * kKeyHalf + key : key;                 // entry of the tile
-        const int stride = is_k ? kKRegion : kVRegion, slot = is_k ? kKSlot : kVSlot;
-        uint8_t *const dst = is_k ? sK + (lane >> 4) * 2 * kKRegion : sV;
+        const int slot = is_k ? kKSlot : kVSlot;
+        uint8_t *const dst = is_k ? sK + (lane >> 3) * kKRegion : sV + (lane >> 4) * kVRegion;
         uint64_t *const full = is_k ? S.k_full : S.v_full, *const empty = is_k ? S.k_empty : S.v_empty;
         bool more = walk.next(a, sg);
-        int kt = sg.k0;
+        int kt = more ? sg.k0 : 0;
         // the cache row of this thread's entry in the next tile of the walk; -2 behind the last tile
         auto next_row = [&]() -> int64_t {
             if (!more) return -2;
@@ -698,7 +717,7 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (!ptx::mbar_wait(&empty[h], ph, abort_flag)) bad = true;
-                store_piece(dst + h * slot, stride, key, x[h]);
+                store_piece(dst + h * slot, key, x[h]);
                 ptx::fence_async_smem();
                 __syncwarp();
                 if (lane == 0) arrive_first(&full[h]);
@@ -724,51 +743,98 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
 // 3. merge: 128 threads per query, 4 channels each
 // ---------------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(128) prefix_merge_kernel(const Args a) {
+    __shared__ float weight[128];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t f = blockIdx.x;                        // row * H + head
-    const int row = (int)(f / a.H);
+    const int row = (int)(f / a.H), t = threadIdx.x;
+    const int64_t total = a.groups[a.G].work0;
+    const float own_nat = a.own_lse ? a.own_lse[f] : -INFINITY;
+    float4 own = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (own_nat != -INFINITY) own = *reinterpret_cast<const float4 *>(a.own_out + f * kLatent + t * 4);
     const int g = find_group(a.groups, a.G, row, [](const Group &x) { return (int64_t)x.row0; });
     const Group gr = a.groups[g];
-    int64_t c0 = 0, c1 = -1, tile = 0;
-    int side = 0, qi = 0;                                // the CTA of the pair, and its query
-    const int64_t total = a.groups[a.G].work0;
+    int n = 0, qi = 0;                                   // pieces of this query's tile; its place in them
+    const float *first = nullptr;                        // the first one's [maximum | sum | output] for this query
     const int64_t nt = (gr.n + kTile - 1) / kTile;
     if (row >= gr.row0 && row < gr.row0 + gr.rows && nt > 0) {
-        const int64_t i = f - (int64_t)gr.row0 * a.H;
-        tile = gr.tile0 + i / kQ;
-        side = (int)(i % kQ) / kQHalf;
+        const int64_t i = f - (int64_t)gr.row0 * a.H, qt = i / kQ;
+        const int side = (int)(i % kQ) / kQHalf;
         qi = (int)(i % kQHalf);
         // the shares that hold work items u0 .. u1 of this query tile; share c begins at total c / shares
-        const int64_t shares = shares_of(a, total), u0 = gr.work0 + (i / kQ) * nt, u1 = u0 + nt - 1;
-        c0 = u0 * shares / total;
+        const int64_t shares = shares_of(a, total), u0 = gr.work0 + qt * nt, u1 = u0 + nt - 1;
+        int64_t c0, c1;
+        if (total < (1 << 20)) {                         // 32-bit divisions where they suffice
+            c0 = (uint32_t)(u0 * shares) / (uint32_t)total;
+            c1 = (uint32_t)(u1 * shares) / (uint32_t)total;
+        } else {
+            c0 = u0 * shares / total;
+            c1 = u1 * shares / total;
+        }
         while (total * (c0 + 1) / shares <= u0) ++c0;
-        c1 = u1 * shares / total;
         while (total * (c1 + 1) / shares <= u1) ++c1;
+        n = (int)(c1 - c0) + 1;
+        first = a.parts + (2 * (c0 + gr.tile0 + qt) + side) * (int64_t)kPartFloats + qi;
     }
+    constexpr int64_t kStep = 2 * (int64_t)kPartFloats;  // from one share's piece to the next's
     constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-    const float own = a.own_lse ? a.own_lse[f] * kLog2e : -INFINITY;
-    float top = own;
-    for (int64_t c = c0; c <= c1; ++c) {
-        const float *p = a.parts + (2 * (c + tile) + side) * (int64_t)kPartFloats;
-        if (p[kQHalf + qi] != 0.0f) top = fmaxf(top, p[qi]);
-    }
+    const float own2 = own_nat * kLog2e;
+    // the largest maximum of the pieces that count and of the own part
+    float top = own2;
+    for (int c = t; c < n; c += 128)
+        if (first[c * kStep + kQHalf] != 0.0f) top = fmaxf(top, first[c * kStep]);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if ((t & 31) == 0) weight[t >> 5] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(weight[0], weight[1]), fmaxf(weight[2], weight[3]));
     float L = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t c = c0; c <= c1; ++c) {
-        const float *p = a.parts + (2 * (c + tile) + side) * (int64_t)kPartFloats;
-        const float ls = p[kQHalf + qi];
-        if (ls == 0.0f) continue;                        // no key of this piece counts
-        const float w = exp2f(p[qi] - top);
-        L += w * ls;
-        const float4 o = *reinterpret_cast<const float4 *>(p + 2 * kQHalf + qi * kLatent + threadIdx.x * 4);
-        acc[0] += w * o.x; acc[1] += w * o.y; acc[2] += w * o.z; acc[3] += w * o.w;
+    const int q_off = 2 * kQHalf + qi * (kLatent - 1) + t * 4;       // of its output, from `first`
+    for (int c0 = 0; c0 < n; c0 += 128) {
+        const int m = min(128, n - c0);
+        __syncthreads();
+        float ls = 0.0f;
+        if (t < m) {
+            const float *p = first + (c0 + t) * kStep;
+            ls = p[kQHalf];
+            weight[t] = ls != 0.0f ? exp2f(p[0] - top) : 0.0f;       // no key of the piece counts: 0
+        }
+        __syncthreads();
+        int c = 0;
+        for (; c + 4 <= m; c += 4) {
+            float4 v[4];
+            float s4[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float *p = first + (c0 + c + k) * kStep;
+                v[k] = *reinterpret_cast<const float4 *>(p + q_off);
+                s4[k] = p[kQHalf];
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float w = weight[c + k];
+                if (s4[k] != 0.0f) {
+                    L += w * s4[k];
+                    acc[0] += w * v[k].x; acc[1] += w * v[k].y; acc[2] += w * v[k].z; acc[3] += w * v[k].w;
+                }
+            }
+        }
+        for (; c < m; ++c) {
+            const float *p = first + (c0 + c) * kStep;
+            const float w = weight[c], s1 = p[kQHalf];
+            if (s1 != 0.0f) {
+                const float4 v = *reinterpret_cast<const float4 *>(p + q_off);
+                L += w * s1;
+                acc[0] += w * v.x; acc[1] += w * v.y; acc[2] += w * v.z; acc[3] += w * v.w;
+            }
+        }
     }
-    if (a.own_out && own != -INFINITY) {
-        const float w = exp2f(own - top);
+    if (own_nat != -INFINITY) {
+        const float w = exp2f(own2 - top);
         L += w;
-        const float4 o = *reinterpret_cast<const float4 *>(a.own_out + f * kLatent + threadIdx.x * 4);
-        acc[0] += w * o.x; acc[1] += w * o.y; acc[2] += w * o.z; acc[3] += w * o.w;
+        acc[0] += w * own.x; acc[1] += w * own.y; acc[2] += w * own.z; acc[3] += w * own.w;
     }
     const float inv = L != 0.0f ? 1.0f / L : 0.0f;       // no key at all: 0; a NaN stays one
-    const int64_t oi = f * kLatent + threadIdx.x * 4;
+    const int64_t oi = f * kLatent + t * 4;
     if (a.out_dtype == CSA2_DTYPE_F32) {
         *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + oi) =
             make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
@@ -778,7 +844,7 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const Args a) {
         o2[1] = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
     }
     __syncthreads();                                     // lse may be own_lse
-    if (a.lse && threadIdx.x == 0) a.lse[f] = L != 0.0f ? (top + log2f(L)) * kLn2 : -INFINITY;
+    if (a.lse && t == 0) a.lse[f] = L != 0.0f ? (top + log2f(L)) * kLn2 : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -845,6 +911,25 @@ inline Layout layout(int rows, int H, int G, int64_t max_n) {
 
 static SmemLimit g_prefix_smem, g_prefix_prep_smem;
 
+// A launch that may begin while the stream's last kernel still runs: it waits itself
+// (griddepcontrol.wait) before it touches anything.
+template <typename... KArgs, typename... Given>
+static cudaError_t launch_after(void (*kernel)(KArgs...), unsigned grid, int threads, int smem, cudaStream_t st,
+                                const Given &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
 size_t prefix_attn_workspace_bytes(int rows, int H, int G, int64_t max_n) { return pfx::layout(rows, H, G, max_n).total; }
 
 cudaError_t launch_prefix_attn(const uint16_t *q, int rows, int H, const int32_t *row_start, int G, const uint8_t *kv,
@@ -899,12 +984,12 @@ cudaError_t launch_prefix_attn(const uint16_t *q, int rows, int H, const int32_t
             return cudaErrorInvalidValue;
         e = ensure_smem_limit(g_prefix_smem, pfx::prefix_attn_kernel, pfx::kSmemBytes);
         if (e != cudaSuccess) return e;
-        pfx::prefix_attn_kernel<<<(unsigned)(2 * l.pairs), pfx::kThreads, pfx::kSmemBytes, st>>>(a, qmap);
-        e = cudaGetLastError();
+        e = launch_after(pfx::prefix_attn_kernel, (unsigned)(2 * l.pairs), pfx::kThreads, pfx::kSmemBytes, st, a, qmap);
         if (e != cudaSuccess) return e;
         launches = 3;
     }
-    pfx::prefix_merge_kernel<<<(unsigned)((int64_t)rows * H), 128, 0, st>>>(a);
+    e = launch_after(pfx::prefix_merge_kernel, (unsigned)((int64_t)rows * H), 128, 0, st, a);
+    if (e != cudaSuccess) return e;
     note_launches(launches);
     return cudaGetLastError();
 }
