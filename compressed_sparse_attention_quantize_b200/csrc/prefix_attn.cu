@@ -43,7 +43,7 @@
 //
 // Roles per CTA: warp 0 copies Q; warps 2 and 3 of the first CTA issue the MMAs of S and of O; warps
 // 4-11 softmax and partials; warps 12-19 entries to K, 20-27 to V (half as many, with twice the
-// channels each: 692 us; their chain of wait, conversion, store and arrival was the longest).
+// channels each, took longer: their chain of wait, conversion, store and arrival was the longest).
 //
 // Bound: MMAs of N=128 take 46 cycles and N=256 60 (measured), 2432 a tile, and the tile's
 // shared-memory traffic (operands 224 KB, K and V 128 KB, P 16 KB) 2900 cycles at 128 bytes a cycle.
@@ -78,11 +78,15 @@ constexpr int kSoftWarps = 8;
 constexpr int kDeqWarp0 = 12;
 constexpr int kDeqWarps = 8;              // for K, and as many for V
 // Registers per thread of the first four warps, the softmax's and the entries': the launch's 72 x 896,
-// dealt out again.
-constexpr int kRegsLaunch = 72, kRegsIssue = 56, kRegsSoft = 96, kRegsDeq = 64;
+// dealt out again.  (128 rows x 64 heads on 32768 entries: 72 / 88 / 64 601 us, 56 / 96 / 64 681 us,
+// 64 / 96 / 56 743 us: what the issuing threads spill costs most.)
+constexpr int kRegsLaunch = 72, kRegsIssue = 72, kRegsSoft = 88, kRegsDeq = 64;
 static_assert(128 * kRegsIssue + 32 * kSoftWarps * kRegsSoft + 64 * kDeqWarps * kRegsDeq <= kThreads * kRegsLaunch &&
                   kThreads * kRegsLaunch <= 65536,
               "a warp group that waited for more registers than there are would wait forever");
+static_assert(kRegsIssue <= kRegsLaunch && kRegsSoft >= kRegsLaunch && kRegsDeq <= kRegsLaunch &&
+                  kRegsIssue % 8 == 0 && kRegsSoft % 8 == 0 && kRegsDeq % 8 == 0,
+              "a decrease that is none, or an increase, is an illegal instruction");
 constexpr int kTmemCols = 512;
 constexpr int kSCols = 64;                 // a buffer of S; two from column 0
 constexpr int kOCol = 128;                 // two accumulators of 128 columns
