@@ -77,16 +77,6 @@ constexpr int kSoftWarp0 = 4;
 constexpr int kSoftWarps = 8;
 constexpr int kDeqWarp0 = 12;
 constexpr int kDeqWarps = 8;              // for K, and as many for V
-// Registers per thread of the first four warps, the softmax's and the entries': the launch's 72 x 896,
-// dealt out again.  (128 rows x 64 heads on 32768 entries: 72 / 88 / 64 601 us, 56 / 96 / 64 681 us,
-// 64 / 96 / 56 743 us: what the issuing threads spill costs most.)
-constexpr int kRegsLaunch = 72, kRegsIssue = 72, kRegsSoft = 88, kRegsDeq = 64;
-static_assert(128 * kRegsIssue + 32 * kSoftWarps * kRegsSoft + 64 * kDeqWarps * kRegsDeq <= kThreads * kRegsLaunch &&
-                  kThreads * kRegsLaunch <= 65536,
-              "a warp group that waited for more registers than there are would wait forever");
-static_assert(kRegsIssue <= kRegsLaunch && kRegsSoft >= kRegsLaunch && kRegsDeq <= kRegsLaunch &&
-                  kRegsIssue % 8 == 0 && kRegsSoft % 8 == 0 && kRegsDeq % 8 == 0,
-              "a decrease that is none, or an increase, is an illegal instruction");
 constexpr int kTmemCols = 512;
 constexpr int kSCols = 64;                 // a buffer of S; two from column 0
 constexpr int kOCol = 128;                 // two accumulators of 128 columns
@@ -324,12 +314,20 @@ struct Ring {
     }
 };
 
-CSA2_D void mma2_f16_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// The descriptors' upper words are the same for all operands here (8-row groups 1024 bytes apart, 128-byte
+// swizzle): only the lower ones, with the address, are kept and stepped.
+CSA2_D void mma2_f16_ss(uint32_t d, uint32_t adesc, uint32_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %5};\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}"
+        ::"r"(d), "r"(adesc), "r"(bdesc), "r"(idesc), "r"(accumulate), "n"(kHigh) : "memory");
+}
+CSA2_D uint32_t desc_low(const void *p, uint32_t lbo_bytes) {
+    return (uint32_t)ptx::sdesc_sw128(ptx::smem_u32(p), lbo_bytes, 1024);
 }
 // Arrives once on `bar` of both CTAs when every MMA issued so far by this thread has completed.
 CSA2_D void commit2(uint64_t *bar) {
@@ -442,7 +440,6 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
     Segment sg;
 
     if (warp < kSoftWarp0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
         if (warp == 0) {
             // ================= copies of Q =================
             if (lane == 0) {
@@ -466,8 +463,8 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
             if (lane == 0 && rank == 0) {
                 // ================= scores: S = Q . V^T =================
                 constexpr uint32_t idesc = ptx::idesc_f16_f32(128, kTile, false, false);
-                const uint64_t q0 = ptx::sdesc_sw128(ptx::smem_u32(sQ), 16, 1024);
-                const uint64_t k0 = ptx::sdesc_sw128(ptx::smem_u32(sK), 16, 1024);
+                const uint32_t q0 = desc_low(sQ, 16);
+                const uint32_t k0 = desc_low(sK, 16);
                 Ring<2> sb;
                 while (ok && walk.next(a, sg)) {
                     if (!ptx::mbar_wait(&S.q_ready, sph, abort_flag)) break;
@@ -481,8 +478,8 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
                             if (!ptx::mbar_wait(&S.k_full[h], kph, abort_flag)) { ok = false; break; }
 #pragma unroll
                             for (int k = 0; k < 16; ++k)
-                                mma2_f16_ss(tmem + sb.st * kSCols, q0 + (uint64_t)((4 * h + (k >> 2)) * (kQRegion >> 4) + (k & 3) * 2),
-                                            k0 + (uint64_t)(h * (kKSlot >> 4) + (k >> 2) * (kKRegion >> 4) + (k & 3) * 2), idesc,
+                                mma2_f16_ss(tmem + sb.st * kSCols, q0 + (uint32_t)((4 * h + (k >> 2)) * (kQRegion >> 4) + (k & 3) * 2),
+                                            k0 + (uint32_t)(h * (kKSlot >> 4) + (k >> 2) * (kKRegion >> 4) + (k & 3) * 2), idesc,
                                             (h | k) != 0);
                             commit2(&S.k_empty[h]);
                         }
@@ -506,9 +503,9 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
                 // A thread of its own: its waits and commits (150 and 60 cycles each, during which a thread's
                 // MMAs stand still) run under the scores' MMAs, and the other way round.
                 constexpr uint32_t idesc = ptx::idesc_f16_f32(128, 256, false, true);
-                const uint64_t p0 = ptx::sdesc_sw128(ptx::smem_u32(sP), 16, 1024);
+                const uint32_t p0 = desc_low(sP, 16);
                 // V read MN-major: 64 channels per 128-byte row, the next 64 one region further
-                const uint64_t v0 = ptx::sdesc_sw128(ptx::smem_u32(sV), kVRegion, 1024);
+                const uint32_t v0 = desc_low(sV, kVRegion);
                 while (ok && walk.next(a, sg)) {
                     // (the first wait for the last segment's accumulators returns at once)
                     if (!ptx::mbar_wait(&S.o_free, sph, abort_flag)) break;
@@ -521,8 +518,8 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
                             if (!ptx::mbar_wait(&S.v_full[i], ph, abort_flag)) { ok = false; break; }
 #pragma unroll
                             for (int k = 0; k < kTile / 16; ++k)
-                                mma2_f16_ss(tmem + kOCol + 128 * i, p0 + (uint64_t)((k >> 2) * (8192 >> 4) + (k & 3) * 2),
-                                            v0 + (uint64_t)(i * (kVSlot >> 4) + k * (2048 >> 4)), idesc,
+                                mma2_f16_ss(tmem + kOCol + 128 * i, p0 + (uint32_t)((k >> 2) * (8192 >> 4) + (k & 3) * 2),
+                                            v0 + (uint32_t)(i * (kVSlot >> 4) + k * (2048 >> 4)), idesc,
                                             (kt > sg.k0 || k > 0) ? 1u : 0u);
                             commit2(&S.v_empty[i]);
                         }
@@ -537,7 +534,6 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
         }
     } else if (warp < kDeqWarp0) {
         // ================= softmax and partials =================
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
         const int sub = warp & 3, hf = (warp - kSoftWarp0) >> 2;
         const int tl = sub * 32 + lane;                  // TMEM lane
         const int row = tl & 63, kh = tl >> 6;           // query; half of the keys (and of the channels)
@@ -562,34 +558,49 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
                 ptx::tc_fence_after();
                 // weights under the maximum so far; a segment's first tile has none yet
                 const uint32_t s_addr = lane_addr + sb.st * kSCols + hf * 32;
-                float p[32];
+                uint32_t w[16];                          // the weights in fp16, two to a word
+                float add;                               // their sum, before the rounding
+                bool over;                               // one of them calls for a larger maximum
                 auto weights = [&]() {
-                    uint32_t u[32];
-                    ptx::tmem_ld32(s_addr, u);
-                    ptx::tmem_ld_wait();
+                    add = 0.0f;
+                    over = false;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) p[i] = ptx::ex2(fmaf(__uint_as_float(u[i]), zs, -mm));
-                    if (mask != 0xFFFFFFFFu) {
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t u[16];
+                        ptx::tmem_ld16(s_addr + 16 * c, u);
+                        ptx::tmem_ld_wait();
+                        float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) p[i] = (mask >> i) & 1u ? p[i] : 0.0f;
+                        for (int i = 0; i < 16; i += 2) {
+                            float p0 = ptx::ex2(fmaf(__uint_as_float(u[i]), zs, -mm));
+                            float p1 = ptx::ex2(fmaf(__uint_as_float(u[i + 1]), zs, -mm));
+                            if (mask != 0xFFFFFFFFu) {
+                                p0 = (mask >> (16 * c + i)) & 1u ? p0 : 0.0f;
+                                p1 = (mask >> (16 * c + i + 1)) & 1u ? p1 : 0.0f;
+                            }
+                            over |= (p0 > kOver) | (p1 > kOver);
+                            sum[0] += p0;
+                            sum[1] += p1;
+                            const __half2 h = __floats2half2_rn(p0, p1);
+                            w[8 * c + (i >> 1)] = *reinterpret_cast<const uint32_t *>(&h);
+                        }
+                        add += sum[0] + sum[1];
                     }
                 };
                 weights();
-                bool over = false;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) over |= p[i] > kOver;
                 float al = 1.0f;
                 // one barrier decides whether to stop and whether some maximum moves
                 if (tc::block_any(over || bad || *abort_flag != 0, bar, 128)) {
                     if (tc::block_any(bad || *abort_flag != 0, bar, 128)) { aborted = true; break; }
                     float top = -INFINITY;
-                    {
-                        uint32_t u[32];
-                        ptx::tmem_ld32(s_addr, u);
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t u[16];
+                        ptx::tmem_ld16(s_addr + 16 * c, u);
                         ptx::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if ((mask >> i) & 1u) top = fmaxf(top, __uint_as_float(u[i]) * zs);
+                        for (int i = 0; i < 16; ++i)
+                            if ((mask >> (16 * c + i)) & 1u) top = fmaxf(top, __uint_as_float(u[i]) * zs);
                     }
                     S.red[kh * 2 + hf][row] = top;
                     ptx::named_barrier(bar, 128);
@@ -605,15 +616,7 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
                 __syncwarp();
                 if (lane == 0) arrive_first(&S.s_free[sb.st]);
                 sb.next();
-                float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                uint32_t w[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    add[i & 3] += p[2 * i] + p[2 * i + 1];
-                    const __half2 h = __floats2half2_rn(p[2 * i], p[2 * i + 1]);
-                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
-                }
-                l += (add[0] + add[1]) + (add[2] + add[3]);
+                l += add;
                 // P and the accumulators are at rest once the last tile's second product is done
                 if (!ptx::mbar_wait(&S.v_empty[1], pph, abort_flag)) bad = true;
                 pph ^= 1;
@@ -626,13 +629,13 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
                     ptx::tc_fence_after();
                     const float f = al == 0.0f ? 1.0f : al;
 #pragma unroll 1
-                    for (int c = 0; c < 128; c += 32) {
-                        uint32_t o[32];
-                        ptx::tmem_ld32(lane_addr + kOCol + 128 * hf + c, o);
+                    for (int c = 0; c < 128; c += 16) {
+                        uint32_t o[16];
+                        ptx::tmem_ld16(lane_addr + kOCol + 128 * hf + c, o);
                         ptx::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        ptx::tmem_st32(lane_addr + kOCol + 128 * hf + c, o);
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        ptx::tmem_st16(lane_addr + kOCol + 128 * hf + c, o);
                     }
                     ptx::tmem_st_wait();
                 }
@@ -688,7 +691,6 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
         // channels 256 h + 64 (lane / 8) ..; V: entry `key` of 128, channels 64 (lane / 16) .. of the CTA's
         // 128 of half h.  Eight neighbouring lanes have neighbouring entries: their 16-byte stores meet
         // no conflicts in the swizzled rows.
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDeq));
         const bool is_k = warp < kDeqWarp0 + kDeqWarps;
         const int dw = (warp - kDeqWarp0) & (kDeqWarps - 1);
         const int key = is_k ? dw * 8 + (lane & 7) : dw * 16 + (lane & 15);
