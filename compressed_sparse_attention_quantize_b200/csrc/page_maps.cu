@@ -22,13 +22,34 @@
 namespace csa2 {
 namespace pm {
 
+// Division of 0 <= n < 2^31 by d >= 1 with a multiplication: for d > 1 and s = ceil(log2 d) - 1,
+// magic = ceil(2^(32+s) / d) < 2^32 has n * (magic * d - 2^(32+s)) < n * 2^(s+1) <= 2^(32+s), so
+// floor(n * magic / 2^(32+s)) is the quotient (the rounded-up reciprocal of Granlund and
+// Montgomery, "Division by invariant integers using multiplication", 1994).
+struct Div {
+    uint32_t d, magic;
+    int shift;
+};
+inline Div make_div(uint32_t d) {
+    Div v{d, 0u, 0};
+    if (d > 1) {
+        int s = 0;
+        while ((2ull << s) < d) ++s;                      // 2^s < d <= 2^(s+1)
+        v.shift = s;
+        v.magic = (uint32_t)(((1ull << (32 + s)) + d - 1) / d);
+    }
+    return v;
+}
+CSA2_D uint32_t div_by(uint32_t n, const Div &v) { return v.d == 1u ? n : __umulhi(n, v.magic) >> v.shift; }
+
 constexpr int kThreads = 256;
 constexpr int kTok = 4;                  // token places per thread: a 16-byte store of positions
 constexpr int kEnt = 2;                  // entry places per thread: a 16-byte store of rows
 
 struct Args {
     const int32_t *old_tokens, *new_tokens;
-    int B, ratio, E, window;
+    int B;
+    Div ratio, E, window;
     int32_t *table;
     int max_pages;
     const int32_t *free_pages;
@@ -44,25 +65,28 @@ struct Args {
     bool vec;                            // 16-byte stores: the maps' bases allow them
 };
 
+CSA2_D int32_t pages_of(const Args &a, int32_t entries) {              // ceil(entries / E)
+    return entries == 0 ? 0 : (int32_t)div_by((uint32_t)(entries - 1), a.E) + 1;
+}
+
 // A request's lengths as the kernel uses them.
 struct Lens {
     int32_t o, n;                        // tokens before and after the step
-    int64_t e0, e1;                      // entries before and after
-    int64_t have, need;                  // pages held, pages to take (both within the table's width)
+    int32_t e0, e1;                      // entries before and after
+    int32_t have, need;                  // pages held, pages to take (both within the table's width)
     bool bad;
 };
-CSA2_D Lens lens_of(const Args &a, int b) {
+CSA2_D Lens lens_from(const Args &a, int32_t o, int32_t n) {
     Lens l;
-    const int32_t o = a.old_tokens[b], n = a.new_tokens[b];
     l.bad = o < 0 || n < o;
     l.o = max(o, 0);
     l.n = max(n, l.o);
-    l.e0 = l.o / a.ratio;
-    l.e1 = l.n / a.ratio;
-    const int64_t have = (l.e0 + a.E - 1) / a.E, want = (l.e1 + a.E - 1) / a.E;
+    l.e0 = (int32_t)div_by((uint32_t)l.o, a.ratio);
+    l.e1 = (int32_t)div_by((uint32_t)l.n, a.ratio);
+    const int32_t have = pages_of(a, l.e0), want = pages_of(a, l.e1);
     l.bad |= want > a.max_pages;
-    l.have = min(have, (int64_t)a.max_pages);
-    l.need = min(want, (int64_t)a.max_pages) - l.have;
+    l.have = min(have, a.max_pages);
+    l.need = min(want, a.max_pages) - l.have;
     return l;
 }
 
@@ -85,48 +109,17 @@ CSA2_D int64_t warp_scan(int64_t v, int lane) {          // inclusive
     return v;
 }
 
+// Shared bytes per request: three offsets, and the lengths.
+constexpr int kSharedPer = 3 * 8 + 2 * 4;
+
 __global__ void __launch_bounds__(kThreads) page_maps_kernel(const Args a) {
     extern __shared__ __align__(16) uint8_t smem[];
     const int B = a.B, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     int64_t *tok = reinterpret_cast<int64_t *>(smem);     // [B + 1] token offsets
     int64_t *ent = tok + B + 1;                           // [B + 1] entry offsets
     int64_t *pag = ent + B + 1;                           // [B + 1] page offsets (needs before b)
+    int32_t *olds = reinterpret_cast<int32_t *>(pag + B + 1), *news = olds + B;
     __shared__ int64_t part[3][kThreads / 32];
-
-    // ---- exclusive scans over the requests: consecutive requests per thread ----
-    const int per = (B + kThreads - 1) / kThreads;
-    const int b0 = min(t * per, B), b1 = min(b0 + per, B);
-    int64_t s[3] = {0, 0, 0};
-    for (int b = b0; b < b1; ++b) {
-        const Lens l = lens_of(a, b);
-        s[0] += l.n - l.o;
-        s[1] += l.e1 - l.e0;
-        s[2] += l.need;
-    }
-    int64_t x[3];
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        x[k] = warp_scan(s[k], lane);
-        if (lane == 31) part[k][warp] = x[k];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        int64_t before = 0;
-        for (int w = 0; w < warp; ++w) before += part[k][w];
-        x[k] += before - s[k];
-    }
-    for (int b = b0; b < b1; ++b) {
-        const Lens l = lens_of(a, b);
-        tok[b] = x[0];
-        ent[b] = x[1];
-        pag[b] = x[2];
-        x[0] += l.n - l.o;
-        x[1] += l.e1 - l.e0;
-        x[2] += l.need;
-    }
-    if (b1 == B && b0 < B) { tok[B] = x[0]; ent[B] = x[1]; pag[B] = x[2]; }
-    __syncthreads();
 
     // pages left in the list, from its position on
     const int32_t next = a.free_next[0];
@@ -134,17 +127,53 @@ __global__ void __launch_bounds__(kThreads) page_maps_kernel(const Args a) {
     const int64_t avail = next_ok ? a.n_free - next : 0;
     const int32_t *fresh = a.free_pages + (next_ok ? next : 0);
 
+    // ---- exclusive scans over the requests, a block's width at a time ----
+    int64_t carry[3] = {0, 0, 0};
+    for (int b0 = 0; b0 < B; b0 += kThreads) {
+        const int b = b0 + t;
+        int64_t s[3] = {0, 0, 0}, x[3];
+        if (b < B) {
+            const int32_t o = a.old_tokens[b], n = a.new_tokens[b];
+            olds[b] = o;
+            news[b] = n;
+            const Lens l = lens_from(a, o, n);
+            s[0] = l.n - l.o;
+            s[1] = l.e1 - l.e0;
+            s[2] = l.need;
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            x[k] = warp_scan(s[k], lane);
+            if (lane == 31) part[k][warp] = x[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            int64_t all = carry[k];
+#pragma unroll
+            for (int w = 0; w < kThreads / 32; ++w) {
+                if (w == warp) x[k] += all - s[k];
+                all += part[k][w];
+            }
+            carry[k] = all;
+        }
+        if (b < B) { tok[b] = x[0]; ent[b] = x[1]; pag[b] = x[2]; }
+        __syncthreads();
+    }
+    if (t == 0) { tok[B] = carry[0]; ent[B] = carry[1]; pag[B] = carry[2]; }
+    __syncthreads();
+
     // ---- per request: a warp each ----
     const int nwarps = gridDim.x * (kThreads / 32);
     for (int b = blockIdx.x * (kThreads / 32) + warp; b < B; b += nwarps) {
-        const Lens l = lens_of(a, b);
-        const int64_t got = min(max(avail - pag[b], (int64_t)0), l.need);
-        for (int64_t k = lane; k < l.need; k += 32)
+        const Lens l = lens_from(a, olds[b], news[b]);
+        const int32_t got = (int32_t)min(max(avail - pag[b], (int64_t)0), (int64_t)l.need);
+        for (int k = lane; k < l.need; k += 32)
             a.table[(int64_t)b * a.max_pages + l.have + k] = k < got ? fresh[pag[b] + k] : -1;
         if (lane == 0) {
             if (l.bad || got < l.need) raise_device_error(CSA2_ERR_SHAPE);
-            a.n_entries[b] = (int32_t)min(l.e1, (l.have + got) * a.E);
-            if (a.swa_len) a.swa_len[b] = min(l.n, a.window);
+            a.n_entries[b] = (int32_t)min((int64_t)l.e1, (int64_t)(l.have + got) * a.E.d);
+            if (a.swa_len) a.swa_len[b] = min(l.n, (int32_t)a.window.d);
             a.token_off[b] = tok[b];
             a.entry_off[b] = ent[b];
         }
@@ -171,16 +200,16 @@ __global__ void __launch_bounds__(kThreads) page_maps_kernel(const Args a) {
                 row[k] = -1;
                 if (i >= ent[B] || i >= a.cap_entries) continue;
                 while (i >= ent[b + 1]) ++b;
-                const Lens l = lens_of(a, b);
-                const int64_t e = l.e0 + (i - ent[b]);
-                const int64_t pi = e / a.E;
+                const Lens l = lens_from(a, olds[b], news[b]);
+                const int32_t e = l.e0 + (int32_t)(i - ent[b]);
+                const int32_t pi = (int32_t)div_by((uint32_t)e, a.E);
                 int32_t page = -1;
                 if (pi < l.have)
                     page = a.table[(int64_t)b * a.max_pages + pi];     // held before this step
-                else if (pi - l.have < min(max(avail - pag[b], (int64_t)0), l.need))
+                else if (pi - l.have < min(max(avail - pag[b], (int64_t)0), (int64_t)l.need))
                     page = fresh[pag[b] + (pi - l.have)];
                 if (page >= 0)
-                    row[k] = (int64_t)page * a.E + (e - pi * a.E);
+                    row[k] = (int64_t)page * a.E.d + (e - pi * (int32_t)a.E.d);
                 else
                     raise_device_error(CSA2_ERR_SHAPE);
             }
@@ -196,27 +225,32 @@ __global__ void __launch_bounds__(kThreads) page_maps_kernel(const Args a) {
         const int64_t i0 = (g - ent_groups) * kTok;
         int64_t row[kTok];
         int32_t pos[kTok];
-        int b = i0 < tok[B] ? find_request(tok, B, i0) : B;
-        int64_t lo = 0, hi = 0;                           // places of request b
-        int32_t o = 0, n = 0;
+        if (i0 >= tok[B]) {                               // behind the last request
 #pragma unroll
-        for (int k = 0; k < kTok; ++k) {
-            const int64_t i = i0 + k;
-            row[k] = -1;
-            pos[k] = -1;
-            if (i >= tok[B]) continue;
-            if (i >= hi) {                                // the first place, or a new request begins
-                while (i >= tok[b + 1]) ++b;
-                lo = tok[b];
-                hi = tok[b + 1];
-                const Lens l = lens_of(a, b);
-                o = l.o;
-                n = l.n;
+            for (int k = 0; k < kTok; ++k) { row[k] = -1; pos[k] = -1; }
+        } else {
+            int b = find_request(tok, B, i0);
+            int64_t lo = 0, hi = 0;                       // places of request b
+            int32_t o = 0, n = 0;
+#pragma unroll
+            for (int k = 0; k < kTok; ++k) {
+                const int64_t i = i0 + k;
+                row[k] = -1;
+                pos[k] = -1;
+                if (i >= tok[B]) continue;
+                if (i >= hi) {                            // the first place, or a new request begins
+                    while (i >= tok[b + 1]) ++b;
+                    lo = tok[b];
+                    hi = tok[b + 1];
+                    o = max(olds[b], 0);
+                    n = max(news[b], o);
+                }
+                const int32_t p = o + (int32_t)(i - lo);
+                pos[k] = p;
+                // a longer step writes its last `window` tokens: earlier ones would share their slots
+                if ((int64_t)p >= (int64_t)n - a.window.d)
+                    row[k] = (int64_t)b * a.window.d + (p - (int32_t)(div_by((uint32_t)p, a.window) * a.window.d));
             }
-            const int32_t p = o + (int32_t)(i - lo);
-            pos[k] = p;
-            // a longer step writes its last `window` tokens: earlier ones would share their slots
-            if (p >= n - a.window) row[k] = (int64_t)b * a.window + p % a.window;
         }
         if (a.vec && i0 + kTok <= a.cap_tokens) {
             if (a.window_rows) {
@@ -237,26 +271,6 @@ __global__ void __launch_bounds__(kThreads) page_maps_kernel(const Args a) {
 }
 
 // ---- entry numbers to rows -------------------------------------------------------------------
-// Division of 0 <= n < 2^31 by d >= 1 with a multiplication: for d > 1 and s = ceil(log2 d) - 1,
-// magic = ceil(2^(32+s) / d) < 2^32 has n * (magic * d - 2^(32+s)) < n * 2^(s+1) <= 2^(32+s), so
-// floor(n * magic / 2^(32+s)) is the quotient (the rounded-up reciprocal of Granlund and
-// Montgomery, "Division by invariant integers using multiplication", 1994).
-struct Div {
-    uint32_t d, magic;
-    int shift;
-};
-inline Div make_div(uint32_t d) {
-    Div v{d, 0u, 0};
-    if (d > 1) {
-        int s = 0;
-        while ((2ull << s) < d) ++s;                      // 2^s < d <= 2^(s+1)
-        v.shift = s;
-        v.magic = (uint32_t)(((1ull << (32 + s)) + d - 1) / d);
-    }
-    return v;
-}
-CSA2_D uint32_t div_by(uint32_t n, const Div &v) { return v.d == 1u ? n : __umulhi(n, v.magic) >> v.shift; }
-
 struct IdArgs {
     const int32_t *ids;
     int T, K;
@@ -323,10 +337,11 @@ cudaError_t launch_page_maps(const int32_t *old_tokens, const int32_t *new_token
                              int64_t *window_rows, int32_t *q_pos, int64_t cap_tokens, cudaStream_t st) {
     const uintptr_t bases = reinterpret_cast<uintptr_t>(entry_rows) | reinterpret_cast<uintptr_t>(window_rows) |
                             reinterpret_cast<uintptr_t>(q_pos);
-    pm::Args a{old_tokens, new_tokens, B, ratio, E, window, table, max_pages, free_pages, n_free, free_next,
+    pm::Args a{old_tokens, new_tokens, B, pm::make_div((uint32_t)ratio), pm::make_div((uint32_t)E),
+               pm::make_div((uint32_t)window), table, max_pages, free_pages, n_free, free_next,
                free_next_out, n_entries, swa_len, entry_off, entry_rows, cap_entries, token_off, window_rows, q_pos,
                cap_tokens, (bases & 15u) == 0};
-    const int smem = 3 * (B + 1) * 8;
+    const int smem = (B + 1) * pm::kSharedPer;
     cudaError_t e = ensure_smem_limit(g_page_maps_smem, pm::page_maps_kernel, smem);
     if (e != cudaSuccess) return e;
     const int64_t groups = ceil_div(cap_entries, pm::kEnt) + (window_rows || q_pos ? ceil_div(cap_tokens, pm::kTok) : 0);
