@@ -83,14 +83,24 @@ struct Ctl {
     int abort_flag;
 };
 
-CSA2_HD constexpr uint32_t idesc_fp4(int N, bool e8m0, int sf_id) {
+CSA2_HD constexpr uint32_t idesc_fp4(int M, int N, bool e8m0, int sf_id) {
     return ((uint32_t)sf_id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((e8m0 ? 1u : 0u) << 23) |
-           ((uint32_t)(kM >> 4) << 24) | ((uint32_t)sf_id << 29);
+           ((uint32_t)(M >> 4) << 24) | ((uint32_t)sf_id << 29);
 }
 
-template <bool MX>
+template <bool MX, bool PAIR>
 CSA2_D void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t acc) {
-    if (MX)
+    if (MX && PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc) : "memory");
+    else if (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.block16 [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc) : "memory");
+    else if (MX)
         asm volatile(
             "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
             "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
@@ -154,10 +164,6 @@ CSA2_D void tma_store_2d(const void *tmap, const void *src, int32_t x, int32_t y
 }
 // This thread's bulk stores have read their shared memory.
 CSA2_D void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-CSA2_D void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 CSA2_D float4 ld_peer4(const float *p, uint32_t rank) {
     uint32_t a;
     float4 v;
@@ -197,6 +203,23 @@ CSA2_D uint4 load_scales(const Operand &o, int64_t row, int b0, int nblk) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Barriers that the MMA issuer waits at are the first CTA's, those it signals with an MMA's completion
+// are in the CTAs of `mask`.
+template <bool PAIR>
+CSA2_D void commit(uint64_t *bar, uint16_t mask) {
+    if (PAIR)
+        ptx::mma_commit_pair(bar, mask);
+    else
+        ptx::mma_commit(bar);
+}
+template <bool PAIR>
+CSA2_D void arrive(uint64_t *bar) {
+    if (PAIR)
+        ptx::mbar_arrive_rank0(bar);
+    else
+        ptx::mbar_arrive(bar);
+}
+
 // A place in the ring of stages: its index and the parity of its round.  (Counters, not i % stages:
 // the divisions of every role's loop took longer than a stage's MMAs.)
 struct Ring {
@@ -213,8 +236,10 @@ struct Ring {
 struct TileAt {
     int64_t l0, r0;
 };
-CSA2_D TileAt tile_at(const Args &a, int64_t t) {
-    return {(t % a.tiles_l) * kM, (t / a.tiles_l) * a.NT};
+// The calling CTA's 128 left rows and the NT right rows of tile t.
+template <bool PAIR>
+CSA2_D TileAt tile_at(const Args &a, int64_t t, int rank) {
+    return {(t % a.tiles_l) * (PAIR ? 2 * kM : kM) + (PAIR ? rank * kM : 0), (t / a.tiles_l) * a.NT};
 }
 
 // `cols` (32 or 16) consecutive columns (right rows r ..) of left row l.
@@ -265,9 +290,10 @@ CSA2_D void store_cols(const Args &a, int64_t l, int64_t r, int cols, const floa
     }
 }
 
-CSA2_D int code_bytes_of(int NT) { return kM * 128 + ((NT * 128 + 1023) & ~1023); }
+// A stage's codes: 128 left rows and `right` right ones.
+CSA2_HD constexpr int code_bytes_of(int right) { return kM * 128 + ((right * 128 + 1023) & ~1023); }
 
-template <bool MX, bool BF16>
+template <bool MX, bool BF16, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
 fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const __grid_constant__ CUtensorMap rmap,
                   const __grid_constant__ CUtensorMap lsmap, const __grid_constant__ CUtensorMap rsmap,
@@ -277,7 +303,8 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
     constexpr int kCells = MX ? 2 : 4;                   // scale words per row and stage
     const int NT = a.NT;
     const int r_groups = NT > 128 ? 2 : 1;               // 128-row groups of the right scales
-    const int code_bytes = code_bytes_of(NT);
+    const int r_codes = PAIR ? NT >> 1 : NT;             // right rows whose codes this CTA holds
+    const int code_bytes = code_bytes_of(r_codes);
     constexpr int kRow = 4 * kCells * kChunk;            // bytes of a scale row in a chunk: 64 or 32
     const int sf_bytes = kRow * 128 * (1 + r_groups);    // a chunk
     // the stages' codes, the epilogue warps' output tiles, the chunks of scales, the barriers
@@ -286,16 +313,19 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
     Ctl &S = *reinterpret_cast<Ctl *>(sf_mem + a.chunks * sf_bytes);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
 
-    const int rank = a.splits > 1 ? (int)(blockIdx.x % a.splits) : 0;
-    const int64_t first = blockIdx.x / a.splits, step = gridDim.x / a.splits;
+    // CTAs of a cluster: the halves of a tile, or the shares of K
+    const int ctas = PAIR ? 2 : a.splits;
+    const int rank = ctas > 1 ? (int)(blockIdx.x % ctas) : 0;
+    const int64_t first = blockIdx.x / ctas, step = gridDim.x / ctas;
     // this CTA's stages: runs of whole 16-byte pieces of a scale row (one stage, or two with E8M0)
     constexpr int kGran = MX ? 2 : 1;
     const int runs = (a.ktiles + kGran - 1) / kGran;
-    const int k0 = kGran * (runs * rank / a.splits), k1 = min(a.ktiles, kGran * (runs * (rank + 1) / a.splits));
+    const int k0 = PAIR ? 0 : kGran * (runs * rank / a.splits);
+    const int k1 = PAIR ? a.ktiles : min(a.ktiles, kGran * (runs * (rank + 1) / a.splits));
 
     if (t == 0) {
         for (int i = 0; i < a.stages; ++i) {
-            ptx::mbar_init(&S.full[i], 1 + 4);
+            ptx::mbar_init(&S.full[i], 1 + (PAIR ? 8 : 4));
             ptx::mbar_init(&S.empty[i], 1);
         }
         for (int i = 0; i < a.chunks; ++i) {
@@ -304,18 +334,24 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&S.acc_full[i], 1);
-            ptx::mbar_init(&S.acc_empty[i], kEpiWarps);
+            ptx::mbar_init(&S.acc_empty[i], PAIR ? 2 * kEpiWarps : kEpiWarps);
         }
         ptx::mbar_init(&S.drain, 1);
         S.abort_flag = 0;
         ptx::fence_async_smem();
+        if (PAIR) ptx::fence_mbar_init();
     }
     if (warp == 0) {
-        ptx::tmem_alloc(&S.tmem_base, a.tmem_cols);
-        ptx::tmem_relinquish();
+        if (PAIR) {
+            ptx::tmem_alloc_pair(&S.tmem_base, a.tmem_cols);
+        } else {
+            ptx::tmem_alloc(&S.tmem_base, a.tmem_cols);
+            ptx::tmem_relinquish();
+        }
     }
     ptx::tc_fence_before();
     __syncthreads();
+    if (PAIR) ptx::cluster_sync();                       // the first CTA's barriers can be arrived at
     ptx::tc_fence_after();
     const uint32_t tmem = S.tmem_base;
     const uint32_t sf_col0 = tmem + a.accs * a.acc_cols;
@@ -329,30 +365,38 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
             int held = 0;                                // stages filled since the last full round
             bool ok = true;
             for (int64_t tile = first; ok && tile < a.tiles; tile += step) {
-                const TileAt at = tile_at(a, tile);
+                const TileAt at = tile_at<PAIR>(a, tile, rank);
                 for (int kt = k0; kt < k1; ++kt) {
                     // (the first round's wait for an earlier round returns at once)
                     if (!ptx::mbar_wait(&S.empty[p.st], p.ph ^ 1, abort_flag)) { ok = false; break; }
                     uint8_t *sl = base + (size_t)p.st * code_bytes, *sr = sl + kM * 128;
-                    ptx::mbar_arrive_expect_tx(&S.full[p.st], (uint32_t)((kM + NT) * 128));
-                    ptx::tma_load_2d(sl, &lmap, kt * 128, (int32_t)at.l0, &S.full[p.st]);
-                    ptx::tma_load_2d(sr, &rmap, kt * 128, (int32_t)at.r0, &S.full[p.st]);
+                    if (PAIR) {
+                        // both CTAs' copies count on the first one's barrier
+                        if (rank == 0) ptx::mbar_arrive_expect_tx(&S.full[p.st], (uint32_t)(2 * (kM + r_codes) * 128));
+                        ptx::tma_load_2d_rank0(sl, &lmap, kt * 128, (int32_t)at.l0, &S.full[p.st]);
+                        ptx::tma_load_2d_rank0(sr, &rmap, kt * 128, (int32_t)at.r0 + rank * r_codes, &S.full[p.st]);
+                    } else {
+                        ptx::mbar_arrive_expect_tx(&S.full[p.st], (uint32_t)((kM + NT) * 128));
+                        ptx::tma_load_2d(sl, &lmap, kt * 128, (int32_t)at.l0, &S.full[p.st]);
+                        ptx::tma_load_2d(sr, &rmap, kt * 128, (int32_t)at.r0, &S.full[p.st]);
+                    }
                     p.next(a.stages);
                     held = min(held + 1, a.stages);
                 }
             }
-            // the copies still in flight land before the CTA leaves: the last use of each stage
+            // the copies still in flight land before the CTA leaves: the last use of each stage (of a
+            // pair, by the MMAs that read it: the second CTA has no barrier of its own for its copies)
             for (; held > 0; --held) {
                 if (p.st == 0) { p.st = a.stages; p.ph ^= 1; }
                 --p.st;
-                ptx::mbar_wait_drain(&S.full[p.st], p.ph);
+                ptx::mbar_wait_drain(PAIR ? &S.empty[p.st] : &S.full[p.st], p.ph);
             }
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ================= MMA issuer =================
-        if (lane == 0) {
-            const uint32_t idesc0 = idesc_fp4(NT, MX, 0), idesc2 = idesc_fp4(NT, MX, 2);
+        // ================= MMA issuer (of a pair: the first CTA's) =================
+        if (lane == 0 && !(PAIR && rank)) {
+            const uint32_t idesc0 = idesc_fp4(PAIR ? 2 * kM : kM, NT, MX, 0), idesc2 = idesc_fp4(PAIR ? 2 * kM : kM, NT, MX, 2);
             const uint64_t da0 = ptx::sdesc_sw128(ptx::smem_u32(base), 16, 1024);
             const uint32_t stage16 = (uint32_t)code_bytes >> 4, l16 = (kM * 128) >> 4;
             Ring p, f, acc;
@@ -375,16 +419,16 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
                         // takes about 150 cycles even when it is over, a stage's MMAs 2 NT
                         if (k == kSteps - 1) seen = ptx::mbar_test(&S.full[p.st], p.ph);
                         const int c = MX ? k >> 1 : k;
-                        mma_fp4<MX>(d, da + 2 * k, db + 2 * k, MX && (k & 1) ? idesc2 : idesc0, sfa + 4 * c,
+                        mma_fp4<MX, PAIR>(d, da + 2 * k, db + 2 * k, MX && (k & 1) ? idesc2 : idesc0, sfa + 4 * c,
                                     sfb + 4 * c * r_groups, (kt > k0 || k > 0) ? 1u : 0u);
                     }
-                    ptx::mma_commit(&S.empty[st]);
+                    commit<PAIR>(&S.empty[st], 3);
                 }
-                if (ok) ptx::mma_commit(&S.acc_full[acc.st]);
+                if (ok) commit<PAIR>(&S.acc_full[acc.st], 3);
                 acc.next(a.accs);
             }
             // every issued MMA has completed before TMEM is released
-            ptx::mma_commit(&S.drain);
+            commit<PAIR>(&S.drain, 1);
             ptx::mbar_wait_drain(&S.drain, 0);
         }
         __syncwarp();
@@ -396,7 +440,7 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
         if (a.sf_tma) {
             if (warp == 2 && lane == 0) {
                 for (int64_t tile = first; ok && tile < a.tiles; tile += step) {
-                    const TileAt at = tile_at(a, tile);
+                    const TileAt at = tile_at<PAIR>(a, tile, rank);
                     for (int kt = k0; kt < k1; kt += kChunk) {
                         if (!ptx::mbar_wait(&S.sf_empty[p.st], p.ph ^ 1, abort_flag)) { ok = false; break; }
                         uint8_t *ss = sf_mem + p.st * sf_bytes;
@@ -418,7 +462,7 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
             const int lt = t - 64;                       // 0 .. 127
             constexpr int kPieces = kRow / 16;           // of a row
             for (int64_t tile = first; ok && tile < a.tiles; tile += step) {
-                const TileAt at = tile_at(a, tile);
+                const TileAt at = tile_at<PAIR>(a, tile, rank);
                 for (int kt = k0; kt < k1; kt += kChunk) {
                     ok = ptx::mbar_wait(&S.sf_empty[p.st], p.ph ^ 1, abort_flag);
                     if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -461,7 +505,7 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&S.full[u.st]);
+                if (lane == 0) arrive<PAIR>(&S.full[u.st]);
                 f.next(a.sf_bufs);
                 u.next(a.stages);
                 back.next(a.stages);
@@ -480,12 +524,12 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
         uint8_t *const stg = store0 + (warp - kEpiWarp0) * kStoreBytes;
         Ring acc;
         for (int64_t tile = first; tile < a.tiles; tile += step) {
-            const TileAt at = tile_at(a, tile);
+            const TileAt at = tile_at<PAIR>(a, tile, rank);
             const bool ok = ptx::mbar_wait(&S.acc_full[acc.st], acc.ph, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) break;
             ptx::tc_fence_after();
             const uint32_t taddr = tmem + lane_base + acc.st * a.acc_cols;
-            if (a.splits > 1) {
+            if (!PAIR && a.splits > 1) {
                 // this CTA's share of K, column by column: every copy into the stages has been
                 // consumed, so their memory is free
                 float *part = reinterpret_cast<float *>(base);
@@ -555,18 +599,18 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
             }
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&S.acc_empty[acc.st]);
+            if (lane == 0) arrive<PAIR>(&S.acc_empty[acc.st]);
             acc.next(a.accs);
         }
         if (lane == 0) ptx::bulk_wait_all();             // the stores have been made before the CTA leaves
         __syncwarp();
     }
-    if (a.splits > 1) {
+    if (!PAIR && a.splits > 1) {
         // every CTA of the cluster gets here, whatever happened before: no wait can be left behind
         __syncwarp();
-        cluster_sync();
+        ptx::cluster_sync();
         if (*abort_flag == 0 && warp >= kEpiWarp0) {
-            const TileAt at = tile_at(a, first);
+            const TileAt at = tile_at<false>(a, first, 0);
             const int et = t - 32 * kEpiWarp0;
             const float *part = reinterpret_cast<const float *>(base);
             const int c0 = NT * rank / a.splits, c1 = NT * (rank + 1) / a.splits;
@@ -599,18 +643,22 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
             }
         }
         __syncwarp();
-        cluster_sync();                                  // peers have read this CTA's shared memory
+        ptx::cluster_sync();                                  // peers have read this CTA's shared memory
     }
     ptx::tc_fence_before();
     __syncthreads();
+    if (PAIR) ptx::cluster_sync();                       // neither CTA's memory is in use any more
     if (warp == 0) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, a.tmem_cols);
+        if (PAIR)
+            ptx::tmem_dealloc_pair(tmem, a.tmem_cols);
+        else
+            ptx::tmem_dealloc(tmem, a.tmem_cols);
     }
 }
 
 struct Plan {
-    bool swap;
+    bool swap, pair;
     int NT, splits, stages, accs, sf_bufs, chunks;
 };
 
@@ -621,65 +669,68 @@ inline int acc_cols_of(int NT) { return NT < 32 ? 32 : NT; }
 // Estimated finish time, in SM cycles, of the candidates (operand order, tile width, K splits); the
 // smallest wins.
 inline Plan make_plan(bool mx, int64_t M, int64_t N, int K, int nsm) {
-    Plan best{false, 128, 1, 4, 2, 2, 2};
+    Plan best{false, false, 128, 1, 4, 2, 2, 2};
     double best_t = 1e300;
     const int ktiles = (K + kKTile - 1) / kKTile;
-    constexpr int widths[5] = {16, 32, 64, 128, 192};
+    constexpr int widths[6] = {16, 32, 64, 128, 192, 256};
     for (int sw = 0; sw < 2; ++sw)
         for (int NT : widths)
             for (int sp = 1; sp <= kMaxSplits; sp *= 2) {
                 const int64_t L = sw ? N : M, R = sw ? M : N;
+                const bool pair = NT == 256;
                 // K is split with tokens as columns only: the shares are then stored along the lanes
                 if (sp > 1 && (!sw || sp > (mx ? (ktiles + 1) / 2 : ktiles) || NT > 128)) continue;
-                const int64_t tiles = ceil_div(L, kM) * ceil_div(R, NT);
+                if (pair && nsm < 2) continue;
+                const int64_t tiles = ceil_div(L, pair ? 2 * kM : kM) * ceil_div(R, NT);
                 const int64_t units = tiles * sp;
                 if (sp > 1 && units > nsm) continue;
                 const double kt = (double)ktiles / sp;
                 // a stage: its MMAs (128 x NT x 64 in NT / 2 cycles) and about 250 cycles around them, or
                 // its bytes through shared memory
-                const double stage = std::max(2.0 * NT + 250.0, (kM + NT) * 144.0 / 48.0);
-                const double waves = (double)ceil_div(units, (int64_t)nsm);
+                const double stage = pair ? 800.0 : std::max(2.0 * NT + 250.0, (kM + NT) * 144.0 / 48.0);
+                const double waves = (double)ceil_div(units, (int64_t)(pair ? nsm / 2 : nsm));
                 const double epi = sw ? 8.0 * NT : 4.0 * NT;
                 // the cluster's sum reads the other CTAs' shared memory at about 12 bytes a cycle
                 const double join = sp > 1 ? 1500.0 + 512.0 * NT * (sp - 1) / sp / 12.0 : 0.0;
                 const double t = 2500.0 + waves * (kt * stage + 800.0 + epi) + join;
                 if (t < best_t) {
                     best_t = t;
-                    best = Plan{sw != 0, NT, sp, 0, 0, 0, 0};
+                    best = Plan{sw != 0, pair, NT, sp, 0, 0, 0, 0};
                 }
             }
     const int NT = best.NT;
-    const int stage = kM * 128 + ((NT * 128 + 1023) & ~1023);
+    const int stage = code_bytes_of(best.pair ? NT / 2 : NT);
     const int room = 227 * 1024 - 1024 - (int)sizeof(Ctl) - kEpiWarps * kStoreBytes;
     best.chunks = NT <= 64 ? kMaxChunks : 2;
     best.stages = std::min(kMaxStages, (room - best.chunks * chunk_bytes_of(mx, NT)) / stage);
-    best.accs = 2;
-    best.sf_bufs = std::min(best.stages, (512 - 2 * acc_cols_of(NT)) / sf_cols_of(mx, NT));
+    best.accs = best.pair ? 1 : 2;
+    best.sf_bufs = std::min(best.stages, (512 - best.accs * acc_cols_of(NT)) / sf_cols_of(mx, NT));
     return best;
 }
 
 }  // namespace fmm
 
-static SmemLimit g_fmm_smem[4];
+static SmemLimit g_fmm_smem[8];
 
-template <bool MX, bool BF16>
+template <bool MX, bool BF16, bool PAIR>
 static cudaError_t launch_fmm(const fmm::Args &a, const CUtensorMap &lm, const CUtensorMap &rm, const CUtensorMap &lsm,
                               const CUtensorMap &rsm, const CUtensorMap &om, int smem, unsigned grid,
                               cudaStream_t st) {
-    cudaError_t e = ensure_smem_limit(g_fmm_smem[(MX ? 2 : 0) + (BF16 ? 1 : 0)], fmm::fp4_matmul_kernel<MX, BF16>, smem);
+    cudaError_t e = ensure_smem_limit(g_fmm_smem[(PAIR ? 4 : 0) + (MX ? 2 : 0) + (BF16 ? 1 : 0)], fmm::fp4_matmul_kernel<MX, BF16, PAIR>, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(fmm::kThreads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = st;
+    const int ctas = PAIR ? 2 : a.splits;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)a.splits;
+    at[0].val.clusterDim.x = (unsigned)ctas;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = a.splits > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, fmm::fp4_matmul_kernel<MX, BF16>, a, lm, rm, lsm, rsm, om);
+    cfg.numAttrs = ctas > 1 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, fmm::fp4_matmul_kernel<MX, BF16, PAIR>, a, lm, rm, lsm, rsm, om);
     note_launches(1);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
@@ -715,7 +766,7 @@ cudaError_t launch_fp4_matmul(int fmt, const uint8_t *a_codes, int64_t a_code_st
     a.right = p.swap ? operand(a_scales, a_scale_stride, M) : operand(b_scales, b_scale_stride, N);
     const uint8_t *lc = p.swap ? b_codes : a_codes, *rc = p.swap ? a_codes : b_codes;
     const int64_t lcs = p.swap ? b_code_stride : a_code_stride, rcs = p.swap ? a_code_stride : b_code_stride;
-    if (!encode(&lm, lc, K / 2, lcs, a.left.rows, fmm::kM, 128) || !encode(&rm, rc, K / 2, rcs, a.right.rows, p.NT, 128))
+    if (!encode(&lm, lc, K / 2, lcs, a.left.rows, fmm::kM, 128) || !encode(&rm, rc, K / 2, rcs, a.right.rows, p.pair ? p.NT / 2 : p.NT, 128))
         return cudaErrorInvalidValue;
     // scale rows by tensor copies where base and stride allow them
     CUtensorMap lsm = lm, rsm = rm;
@@ -732,7 +783,7 @@ cudaError_t launch_fp4_matmul(int fmt, const uint8_t *a_codes, int64_t a_code_st
     a.NT = p.NT;
     a.stages = p.stages;
     a.splits = p.splits;
-    a.tiles_l = (int)ceil_div(a.left.rows, (int64_t)fmm::kM);
+    a.tiles_l = (int)ceil_div(a.left.rows, (int64_t)(p.pair ? 2 * fmm::kM : fmm::kM));
     a.tiles = (int64_t)a.tiles_l * ceil_div(a.right.rows, (int64_t)p.NT);
     a.ktiles = (K + fmm::kKTile - 1) / fmm::kKTile;
     a.accs = p.accs;
@@ -763,14 +814,17 @@ cudaError_t launch_fp4_matmul(int fmt, const uint8_t *a_codes, int64_t a_code_st
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             a.out_tma = false;
     }
-    const int smem = p.stages * (fmm::kM * 128 + ((p.NT * 128 + 1023) & ~1023)) + p.chunks * fmm::chunk_bytes_of(mx, p.NT) +
+    const int smem = p.stages * fmm::code_bytes_of(p.pair ? p.NT / 2 : p.NT) + p.chunks * fmm::chunk_bytes_of(mx, p.NT) +
                      (a.out_tma ? fmm::kEpiWarps * fmm::kStoreBytes : 0) + (int)sizeof(fmm::Ctl) + 1024;
-    const int64_t grid = p.splits > 1 ? a.tiles * p.splits : std::min<int64_t>(a.tiles, device_sm_count());
-    if (mx)
-        return out_dtype == CSA2_DTYPE_BF16 ? launch_fmm<true, true>(a, lm, rm, lsm, rsm, om, smem, (unsigned)grid, st)
-                                            : launch_fmm<true, false>(a, lm, rm, lsm, rsm, om, smem, (unsigned)grid, st);
-    return out_dtype == CSA2_DTYPE_BF16 ? launch_fmm<false, true>(a, lm, rm, lsm, rsm, om, smem, (unsigned)grid, st)
-                                        : launch_fmm<false, false>(a, lm, rm, lsm, rsm, om, smem, (unsigned)grid, st);
+    const int64_t grid = p.pair ? 2 * std::min<int64_t>(a.tiles, device_sm_count() / 2)
+                                : p.splits > 1 ? a.tiles * p.splits : std::min<int64_t>(a.tiles, device_sm_count());
+    const bool bf16 = out_dtype == CSA2_DTYPE_BF16;
+    auto go = [&](auto launch) { return launch(a, lm, rm, lsm, rsm, om, smem, (unsigned)grid, st); };
+    if (p.pair)
+        return mx ? (bf16 ? go(launch_fmm<true, true, true>) : go(launch_fmm<true, false, true>))
+                  : (bf16 ? go(launch_fmm<false, true, true>) : go(launch_fmm<false, false, true>));
+    return mx ? (bf16 ? go(launch_fmm<true, true, false>) : go(launch_fmm<true, false, false>))
+              : (bf16 ? go(launch_fmm<false, true, false>) : go(launch_fmm<false, false, false>));
 }
 
 }  // namespace csa2

@@ -329,25 +329,6 @@ CSA2_D void mma2_f16_ss(uint32_t d, uint32_t adesc, uint32_t bdesc, uint32_t ide
 CSA2_D uint32_t desc_low(const void *p, uint32_t lbo_bytes) {
     return (uint32_t)ptx::sdesc_sw128(ptx::smem_u32(p), lbo_bytes, 1024);
 }
-// Arrives once on `bar` of both CTAs when every MMA issued so far by this thread has completed.
-CSA2_D void commit2(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 ::"r"(ptx::smem_u32(bar)), "h"((uint16_t)3) : "memory");
-}
-// On the first CTA's copy of `bar`.  What an arrival hands over is read by the tensor core of the
-// arriving thread's own SM (operands in its shared memory, behind a proxy fence or a completed copy;
-// its TMEM, behind a tcgen05 fence), so the barriers keep their default scope: with .release.cluster
-// and .acquire.cluster an arrival took 1250 cycles and a wait that was over 450, and the kernel 40%
-// longer than one CTA per 64 queries.
-CSA2_D void arrive_first(uint64_t *bar) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(ptx::smem_u32(bar)));
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
-}
-CSA2_D void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 
 // 64 channels of an entry: 32 bytes of codes and 4 scales.  No entry (row < 0): zeros.  The loads are
 // volatile so that they stay where they are issued, a tile ahead of their use.
@@ -420,16 +401,12 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
         ptx::mbar_init(&S.drain, 2);
         S.abort_flag = 0;
         ptx::fence_async_smem();
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        ptx::fence_mbar_init();
     }
-    if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
-                     ::"r"(ptx::smem_u32(&S.tmem_base)), "r"((uint32_t)kTmemCols) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-    }
+    if (warp == 2) ptx::tmem_alloc_pair(&S.tmem_base, kTmemCols);
     ptx::tc_fence_before();
     __syncthreads();
-    cluster_sync();
+    ptx::cluster_sync();
     ptx::tc_fence_after();
     const uint32_t tmem = S.tmem_base;
     volatile int *abort_flag = &S.abort_flag;
@@ -452,7 +429,7 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
                         ptx::tma_load_2d(sQ + r * kQRegion, &qmap, r * kRegion, (int32_t)(sg.tile * kQ) + rank * kQHalf, &S.q_full);
                     // (also so that no copy is in flight when the CTA leaves)
                     if (!ptx::mbar_wait_drain(&S.q_full, ph)) break;
-                    arrive_first(&S.q_ready);
+                    ptx::mbar_arrive_rank0(&S.q_ready);
                     ph ^= 1;
                 }
             }
@@ -481,17 +458,17 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
                                 mma2_f16_ss(tmem + sb.st * kSCols, q0 + (uint32_t)((4 * h + (k >> 2)) * (kQRegion >> 4) + (k & 3) * 2),
                                             k0 + (uint32_t)(h * (kKSlot >> 4) + (k >> 2) * (kKRegion >> 4) + (k & 3) * 2), idesc,
                                             (h | k) != 0);
-                            commit2(&S.k_empty[h]);
+                            ptx::mma_commit_pair(&S.k_empty[h], 3);
                         }
                         if (!ok) break;
                         kph ^= 1;
-                        commit2(&S.s_full[sb.st]);
+                        ptx::mma_commit_pair(&S.s_full[sb.st], 3);
                         sb.next();
                     }
-                    if (ok) commit2(&S.q_empty);
+                    if (ok) ptx::mma_commit_pair(&S.q_empty, 3);
                 }
                 // every issued MMA has completed before TMEM is released
-                commit2(&S.drain);
+                ptx::mma_commit_pair(&S.drain, 3);
                 ptx::mbar_wait_drain(&S.drain, 0);
             }
             __syncwarp();
@@ -521,13 +498,13 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
                                 mma2_f16_ss(tmem + kOCol + 128 * i, p0 + (uint32_t)((k >> 2) * (8192 >> 4) + (k & 3) * 2),
                                             v0 + (uint32_t)(i * (kVSlot >> 4) + k * (2048 >> 4)), idesc,
                                             (kt > sg.k0 || k > 0) ? 1u : 0u);
-                            commit2(&S.v_empty[i]);
+                            ptx::mma_commit_pair(&S.v_empty[i], 3);
                         }
                         ph ^= 1;
                     }
-                    if (ok) commit2(&S.seg_done);
+                    if (ok) ptx::mma_commit_pair(&S.seg_done, 3);
                 }
-                commit2(&S.drain);
+                ptx::mma_commit_pair(&S.drain, 3);
                 ptx::mbar_wait_drain(&S.drain, 0);
             }
             __syncwarp();
@@ -614,7 +591,7 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
                 }
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_first(&S.s_free[sb.st]);
+                if (lane == 0) ptx::mbar_arrive_rank0(&S.s_free[sb.st]);
                 sb.next();
                 l += add;
                 // P and the accumulators are at rest once the last tile's second product is done
@@ -642,7 +619,7 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
                 ptx::fence_async_smem();
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_first(&S.p_full);
+                if (lane == 0) ptx::mbar_arrive_rank0(&S.p_full);
             }
             if (aborted) break;
             // ---- the segment's partial ----
@@ -681,7 +658,7 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
             }
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_first(&S.o_free);
+            if (lane == 0) ptx::mbar_arrive_rank0(&S.o_free);
             ptx::named_barrier(bar, 128);                // the sums are read before the next maxima are written
         }
     }
@@ -726,7 +703,7 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
                 store_piece(dst + h * slot, key, x[h]);
                 ptx::fence_async_smem();
                 __syncwarp();
-                if (lane == 0) arrive_first(&full[h]);
+                if (lane == 0) ptx::mbar_arrive_rank0(&full[h]);
                 load_piece(a, row1, 256 * h + chan, x[h]);
             }
             if (__any_sync(0xffffffffu, bad)) break;
@@ -738,10 +715,10 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
     __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();
-    cluster_sync();                                      // neither CTA's memory is in use any more
+    ptx::cluster_sync();                                      // neither CTA's memory is in use any more
     if (warp == 2) {
         ptx::tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)kTmemCols) : "memory");
+        ptx::tmem_dealloc_pair(tmem, kTmemCols);
     }
 }
 

@@ -203,6 +203,46 @@ CSA2_D void mma_commit(uint64_t *bar) {
                  ::"r"(smem_u32(bar)) : "memory");
 }
 
+// ---- a pair of CTAs (a cluster of 2 whose MMAs are cta_group::2, issued by the first) ----
+CSA2_D void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+CSA2_D void fence_mbar_init() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
+// Whole warp, of both CTAs; gives up the right to further allocations.
+CSA2_D void tmem_alloc_pair(uint32_t *dst, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                 ::"r"(smem_u32(dst)), "r"(ncols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+CSA2_D void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// The same barrier of the cluster's first CTA.
+CSA2_D uint32_t rank0_u32(const uint64_t *bar) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
+    return a;
+}
+// What an arrival announces to the MMA issuer is read by the tensor core only (the CTA's own shared
+// memory, behind a proxy fence, or its TMEM, behind a tcgen05 fence), so the barriers keep their
+// default scope: with .release.cluster and .acquire.cluster an arrival took 1250 cycles and a wait
+// that was over 450.
+CSA2_D void mbar_arrive_rank0(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(rank0_u32(bar)) : "memory");
+}
+// Completion of the pair's MMAs so far, to the barriers of the CTAs of `mask`.
+CSA2_D void mma_commit_pair(uint64_t *bar, uint16_t mask) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(smem_u32(bar)), "h"(mask) : "memory");
+}
+// A tensor copy into the calling CTA's shared memory that counts on the first CTA's barrier.
+CSA2_D void tma_load_2d_rank0(void *dst, const void *tmap, int32_t x, int32_t y, const uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_u32(dst)), "l"(tmap), "r"(x), "r"(y), "r"(rank0_u32(bar)) : "memory");
+}
+
 // ---------------------------------------------------------------------------------------
 // descriptors
 // ---------------------------------------------------------------------------------------
