@@ -3,10 +3,12 @@
 // with E2M1 codes and one E4M3 scale per 16 channels or one E8M0 scale per 32, both operands as
 // csa2_quantize_kv leaves them (rows of codes, rows of scale bytes), fp32 accumulation.
 //
-// One tile = 128 rows of the "left" matrix (the MMA's M: TMEM lanes) x NT rows of the "right" one
+// One tile of one CTA = 128 rows of the "left" matrix (the MMA's M: TMEM lanes) x NT rows of the "right" one
 // (the MMA's N: TMEM columns).  Left and right are A and B, or B and A when there are few rows in
 // A (a decode batch): then the weights fill the 128 lanes and the batch takes NT = 16 .. 64
-// columns, instead of padding the batch to 128 rows.  Per 256 channels (a stage):
+// columns, instead of padding the batch to 128 rows.  Large products take 256 x 256 tiles by pairs of
+// CTAs (cta_group::2): a CTA holds the codes and scales of its own 128 left rows, the codes of 128 of
+// the right rows and the scales of all 256, and its half of the tile in TMEM.  Per 256 channels (a stage):
 //   warp 0        the codes of both operands by tensor copies (128-byte rows, 128-byte swizzle; rows
 //                 and channels past the end arrive as zeros)
 //   warp 2        the scale bytes of four stages at a time (64 or 32 a row) by tensor copies, two to
@@ -17,17 +19,23 @@
 //   warps 6-9     the scales from shared memory to TMEM: the MMA wants word j (4 scales) of row r in
 //                 lane r % 32, column 4 j + r / 32, repeated in all four lane quarters; each warp writes
 //                 its quarter.  (tcgen05.cp does it from one thread, but queues with the MMAs: 151 us
-//                 for that product with its 12 copies a stage, 54 us without.)
-//   warp 1        one thread: four MMAs a stage (kind::mxf4nvf4 with 16-channel, kind::mxf4 with
-//                 32-channel scales; K = 64 each) into one of two accumulators
-//   warps 10-17   epilogue of the other accumulator: TMEM -> registers -> shared memory -> tensor
-//                 store (direct stores where the output's rows are not 16-byte aligned, or tokens are
-//                 columns)
+//                 for that product with its 12 copies a stage and NT = 192, 54 us without scales.)
+//   warp 1        one thread (of a pair: the first CTA's): four MMAs a stage (kind::mxf4nvf4 with
+//                 16-channel, kind::mxf4 with 32-channel scales; K = 64 each) into an accumulator
+//   warps 10-17   epilogue: TMEM -> registers -> shared memory -> tensor store (direct stores where the
+//                 output's rows are not 16-byte aligned, or tokens are columns)
 // A CTA walks over tiles; everything up to the MMAs of the next tile runs while the epilogue drains
 // the last.  NT = 192 is the widest tile whose two accumulators leave TMEM columns for two stages of
-// scales (2 x 192 + 2 x 48 <= 512).  Few tiles and a long K are split over a cluster: each CTA takes a run of stages, leaves
-// its fp32 tile in its shared memory, and every CTA adds up a share of the columns over the
-// cluster in rank order (no second launch, no atomics: the result does not depend on timing).
+// scales (2 x 192 + 2 x 48 <= 512).  A pair has one accumulator of 256 columns and up to 5 stages of scales.
+// Few tiles and a long K are split over a cluster: each CTA takes a run of stages, leaves its fp32
+// tile in its shared memory, and every CTA adds up a share of the columns over the cluster in rank
+// order (no second launch, no atomics: the result does not depend on timing).
+//
+// Bound of large products: shared memory at 128 bytes a cycle.  A CTA of 128 x 192 writes and reads
+// 40 KB of codes a stage, writes 6 and reads 24 KB of scales (every lane quarter of TMEM needs them
+// all): 880 cycles for 192 columns (1006 measured, 87 us for 4096 x 8192 x 4096 with E4M3 scales); one of
+// a pair 32 KB of codes and 30 of scales, 750 for 256 columns (65 us, 4.2 PFLOP/s, of which the MMAs'
+// wait for the epilogue is 8; sustained, the power limit makes it 75).  Decode batches: the weights' bytes.
 // Every wait is bounded: on expiry the CTA records CSA2_ERR_TIMEOUT, drains, frees TMEM and exits.
 #include "common.cuh"
 #include "tc_ptx.cuh"
@@ -680,16 +688,17 @@ inline Plan make_plan(bool mx, int64_t M, int64_t N, int K, int nsm) {
                 const bool pair = NT == 256;
                 // K is split with tokens as columns only: the shares are then stored along the lanes
                 if (sp > 1 && (!sw || sp > (mx ? (ktiles + 1) / 2 : ktiles) || NT > 128)) continue;
-                if (pair && nsm < 2) continue;
+                if (pair && (sw || nsm < 2)) continue;                 // square tiles: either order is the same
                 const int64_t tiles = ceil_div(L, pair ? 2 * kM : kM) * ceil_div(R, NT);
                 const int64_t units = tiles * sp;
                 if (sp > 1 && units > nsm) continue;
                 const double kt = (double)ktiles / sp;
                 // a stage: its MMAs (128 x NT x 64 in NT / 2 cycles) and about 250 cycles around them, or
-                // its bytes through shared memory
+                // its bytes through shared memory; a pair's was measured
                 const double stage = pair ? 800.0 : std::max(2.0 * NT + 250.0, (kM + NT) * 144.0 / 48.0);
                 const double waves = (double)ceil_div(units, (int64_t)(pair ? nsm / 2 : nsm));
-                const double epi = sw ? 8.0 * NT : 4.0 * NT;
+                // a pair's MMAs wait while its accumulator is read
+                const double epi = pair ? 3000.0 : sw ? 8.0 * NT : 4.0 * NT;
                 // the cluster's sum reads the other CTAs' shared memory at about 12 bytes a cycle
                 const double join = sp > 1 ? 1500.0 + 512.0 * NT * (sp - 1) / sp / 12.0 : 0.0;
                 const double t = 2500.0 + waves * (kt * stage + 800.0 + epi) + join;
@@ -800,9 +809,11 @@ cudaError_t launch_fp4_matmul(int fmt, const uint8_t *a_codes, int64_t a_code_st
     a.out_stride = out_stride;
     const int64_t es = out_dtype == CSA2_DTYPE_BF16 ? 2 : 4;
     a.out_vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && (out_stride * es) % 16 == 0;
-    // whole pieces of 128 bytes along n leave by tensor stores; their rows have to be 16-byte aligned
+    // whole pieces of 128 bytes along n leave by tensor stores; their rows have to be 16-byte aligned and
+    // end at a multiple of 16 bytes: a tensor store that is cut off by the matrix's end still writes the
+    // 16 bytes that the last element lies in
     CUtensorMap om = lm;
-    a.out_tma = !p.swap && p.splits == 1 && p.NT % (es == 2 ? 64 : 32) == 0 && a.out_vec;
+    a.out_tma = !p.swap && p.splits == 1 && p.NT % (es == 2 ? 64 : 32) == 0 && a.out_vec && (N * es) % 16 == 0;
     if (a.out_tma) {
         const cuuint64_t dim[2] = {(cuuint64_t)N, (cuuint64_t)M};
         const cuuint64_t strides[1] = {(cuuint64_t)(out_stride * es)};

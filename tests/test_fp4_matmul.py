@@ -104,6 +104,16 @@ def test_matmul_strides(M, N, K, fmt, code_pad, scale_pad, out_pad, shift):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt", [csa2.FMT_FP4, csa2.FMT_MXFP4])
+@pytest.mark.parametrize("M,N,K,code_pad,scale_pad,out_pad,shift", [
+    (1025, 3330, 2080, 0, 0, 0, 0), (1400, 2561, 4096, 16, 0, 7, 8), (3330, 1100, 2048, 0, 5, 0, 3), (2304, 2048, 1600, 0, 16, 2, 0)])
+def test_matmul_large(M, N, K, code_pad, scale_pad, out_pad, shift, fmt):
+    """Sizes that fill the GPU with 256 x 256 tiles, ragged in every direction."""
+    for dt in (csa2.DTYPE_F32, csa2.DTYPE_BF16):
+        check(M, N, K, fmt, dt, code_pad=code_pad, scale_pad=scale_pad, out_pad=out_pad, shift=shift, wild=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [csa2.FMT_FP4, csa2.FMT_MXFP4])
 def test_matmul_every_scale(fmt):
     """Scales over their whole range, zero and subnormal ones among them."""
     check(40, 300, 1024, fmt, csa2.DTYPE_F32, wild=True)
@@ -111,10 +121,9 @@ def test_matmul_every_scale(fmt):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt", [csa2.FMT_FP4, csa2.FMT_MXFP4])
-@pytest.mark.parametrize("M", [4, 300])
-def test_matmul_nan_scale(fmt, M):
+@pytest.mark.parametrize("M,N,K", [(4, 200, 288), (300, 200, 288), (1200, 3100, 2080)])
+def test_matmul_nan_scale(fmt, M, N, K):
     """A NaN scale spoils its row (column) and nothing else, past the ragged ends included."""
-    N, K = 200, 288
     g = torch.Generator().manual_seed(3)
     a, sa = operand(g, M, K, fmt)
     b, sb = operand(g, N, K, fmt)
