@@ -28,6 +28,13 @@ constexpr int kIndexDim = 64;
 // E4M3 ("fn": bias 7, max 448, no inf) and E2M1
 // ---------------------------------------------------------------------------------------
 
+// Launches that overlap the end of the stream's last kernel (programmatic dependent launch): a kernel
+// launched with launch_after begins once every CTA of the kernel before it has called
+// grid_launch_next (or has ended), and calls grid_wait_last, which returns when that kernel is
+// complete and its writes are visible, before it touches anything.
+CSA2_D void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+CSA2_D void grid_wait_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Decode an E4M3 code to fp32 (exact).
 CSA2_D float e4m3_to_f32(uint32_t code) {
     uint32_t e = (code >> 3) & 15u, m = code & 7u;
@@ -163,5 +170,27 @@ inline cudaError_t ensure_smem_limit(SmemLimit &lim, Kernel kernel, int bytes) {
 
 // Host-side count of kernel launches (csa2_launch_count); every launcher adds its launches.
 void note_launches(int n);
+
+// Launches `kernel` so that it may begin while the stream's last kernel still runs (it calls
+// grid_wait_last itself), in clusters of `cluster` CTAs if that is more than 1.
+template <typename... KArgs, typename... Given>
+inline cudaError_t launch_after(void (*kernel)(KArgs...), unsigned grid, int threads, int smem, int cluster, cudaStream_t st,
+                                const Given &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
 
 }  // namespace csa2

@@ -360,6 +360,7 @@ fp4_matmul_kernel(const Args a, const __grid_constant__ CUtensorMap lmap, const 
     ptx::tc_fence_before();
     __syncthreads();
     if (PAIR) ptx::cluster_sync();                       // the first CTA's barriers can be arrived at
+    grid_wait_last();                                    // everything above ran beside the kernel before
     ptx::tc_fence_after();
     const uint32_t tmem = S.tmem_base;
     const uint32_t sf_col0 = tmem + a.accs * a.acc_cols;
@@ -727,21 +728,9 @@ static cudaError_t launch_fmm(const fmm::Args &a, const CUtensorMap &lm, const C
                               cudaStream_t st) {
     cudaError_t e = ensure_smem_limit(g_fmm_smem[(PAIR ? 4 : 0) + (MX ? 2 : 0) + (BF16 ? 1 : 0)], fmm::fp4_matmul_kernel<MX, BF16, PAIR>, smem);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(fmm::kThreads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = st;
-    const int ctas = PAIR ? 2 : a.splits;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)ctas;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = ctas > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, fmm::fp4_matmul_kernel<MX, BF16, PAIR>, a, lm, rm, lsm, rsm, om);
+    e = launch_after(fmm::fp4_matmul_kernel<MX, BF16, PAIR>, grid, fmm::kThreads, smem, PAIR ? 2 : a.splits, st, a, lm, rm, lsm, rsm, om);
     note_launches(1);
-    return e == cudaSuccess ? cudaGetLastError() : e;
+    return e;
 }
 
 cudaError_t launch_fp4_matmul(int fmt, const uint8_t *a_codes, int64_t a_code_stride, const uint8_t *a_scales,

@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(const Args a)
     extern __shared__ __align__(16) uint8_t smem[];
     Group *gr = reinterpret_cast<Group *>(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_launch_next();
     if (warp == 0) scan_groups(a, gr, lane, blockIdx.x == 0);
     __syncthreads();
     if (blockIdx.x == 0)
@@ -411,8 +411,8 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
     const uint32_t tmem = S.tmem_base;
     volatile int *abort_flag = &S.abort_flag;
     // everything above runs beside the first launch; its results are there from here on
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_wait_last();
+    grid_launch_next();
     Walk walk = walk_of(a, pair);                        // (may be empty: every role's loop then is)
     Segment sg;
 
@@ -727,7 +727,7 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
 // ---------------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(128) prefix_merge_kernel(const Args a) {
     __shared__ float weight[128];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_wait_last();
     const int64_t f = blockIdx.x;                        // row * H + head
     const int row = (int)(f / a.H), t = threadIdx.x;
     const int64_t total = a.groups[a.G].work0;
@@ -894,25 +894,6 @@ inline Layout layout(int rows, int H, int G, int64_t max_n) {
 
 static SmemLimit g_prefix_smem, g_prefix_prep_smem;
 
-// A launch that may begin while the stream's last kernel still runs: it waits itself
-// (griddepcontrol.wait) before it touches anything.
-template <typename... KArgs, typename... Given>
-static cudaError_t launch_after(void (*kernel)(KArgs...), unsigned grid, int threads, int smem, cudaStream_t st,
-                                const Given &...args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-    return e == cudaSuccess ? cudaGetLastError() : e;
-}
-
 size_t prefix_attn_workspace_bytes(int rows, int H, int G, int64_t max_n) { return pfx::layout(rows, H, G, max_n).total; }
 
 cudaError_t launch_prefix_attn(const uint16_t *q, int rows, int H, const int32_t *row_start, int G, const uint8_t *kv,
@@ -967,11 +948,11 @@ cudaError_t launch_prefix_attn(const uint16_t *q, int rows, int H, const int32_t
             return cudaErrorInvalidValue;
         e = ensure_smem_limit(g_prefix_smem, pfx::prefix_attn_kernel, pfx::kSmemBytes);
         if (e != cudaSuccess) return e;
-        e = launch_after(pfx::prefix_attn_kernel, (unsigned)(2 * l.pairs), pfx::kThreads, pfx::kSmemBytes, st, a, qmap);
+        e = launch_after(pfx::prefix_attn_kernel, (unsigned)(2 * l.pairs), pfx::kThreads, pfx::kSmemBytes, 1, st, a, qmap);
         if (e != cudaSuccess) return e;
         launches = 3;
     }
-    e = launch_after(pfx::prefix_merge_kernel, (unsigned)((int64_t)rows * H), 128, 0, st, a);
+    e = launch_after(pfx::prefix_merge_kernel, (unsigned)((int64_t)rows * H), 128, 0, 1, st, a);
     if (e != cudaSuccess) return e;
     note_launches(launches);
     return cudaGetLastError();

@@ -203,6 +203,8 @@ CSA2_D uint32_t quantize_lane8(const float (&v)[8], uint32_t &scale) {
 // without gaps and in place order, so that piece t is at 8 t: no division by the row length.
 // Measured at 4096 rows of 4096 bf16 channels (E4M3 / E8M0 scales): one piece a thread with the rows'
 // division and the comparisons per code 25.9 / 24.9 us; conversions 16.1 / 13.6 us.
+// A product of the rows may begin its set-up when the last CTA has started (its CTAs need a whole
+// SM's registers, so not before).
 constexpr int kPieces = 4;
 template <typename T, int FMT, bool kDense>
 __global__ void __launch_bounds__(256)
@@ -212,6 +214,7 @@ quant_fp4_rows_kernel(const T *__restrict__ x, int64_t rows, int dim, int64_t x_
     constexpr int kLanes = FMT == CSA2_FMT_MXFP4_E2M1_E8M0S32 ? 4 : 2;   // lanes of a block
     const uint32_t per_row = (uint32_t)dim >> 3;
     const int64_t total = rows * (int64_t)per_row;
+    grid_launch_next();
     for (int64_t base = (int64_t)blockIdx.x * (256 * kPieces); base < total; base += (int64_t)gridDim.x * (256 * kPieces)) {
         float v[kPieces][8];
         int64_t d[kPieces], at[kPieces];                 // destination row (-1: none), piece of the row
