@@ -202,10 +202,12 @@ CSA2_D uint32_t quantize_lane8(const float (&v)[8], uint32_t &scale) {
 // memory: x is read once and 4.25 or 4.5 bits per channel are written.  kDense: rows, codes and scales
 // without gaps and in place order, so that piece t is at 8 t: no division by the row length.
 // Measured at 4096 rows of 4096 bf16 channels (E4M3 / E8M0 scales): one piece a thread with the rows'
-// division and the comparisons per code 25.9 / 24.9 us; conversions 16.1 / 13.6 us.
+// division and the comparisons per code 25.9 / 24.9 us; with conversions 16.1 / 13.6; dense 13.0 / 12.1
+// with 1 piece, 12.8 / 10.2 with 2, 13.5 / 9.6 with 4 (4 took 0.6 us more at 32 rows, and the product
+// that follows 1 us more at 4096).
 // A product of the rows may begin its set-up when the last CTA has started (its CTAs need a whole
 // SM's registers, so not before).
-constexpr int kPieces = 4;
+constexpr int kPieces = 2;
 template <typename T, int FMT, bool kDense>
 __global__ void __launch_bounds__(256)
 quant_fp4_rows_kernel(const T *__restrict__ x, int64_t rows, int dim, int64_t x_stride,
