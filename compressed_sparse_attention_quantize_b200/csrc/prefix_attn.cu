@@ -112,7 +112,7 @@ struct Args {
     float *lse;
     // workspace
     Group *groups;                         // [G + 1]
-    int64_t *erow;                         // [G][n_pad]: cache rows of the entries, -1: none
+    int32_t *erow;                         // [G][n_pad]: cache rows of the entries, -1: none
     uint8_t *valid;                        // [G][n_pad]: 1 where there is one
     __half *qh;                            // [tiles][128][512]
     float *qs;                             // [tiles][128]: logit per unit of S
@@ -330,38 +330,40 @@ CSA2_D uint32_t desc_low(const void *p, uint32_t lbo_bytes) {
     return (uint32_t)ptx::sdesc_sw128(ptx::smem_u32(p), lbo_bytes, 1024);
 }
 
-// 64 channels of an entry: 32 bytes of codes and 4 scales.  No entry (row < 0): zeros.  The loads are
-// volatile so that they stay where they are issued, a tile ahead of their use.
+// What a thread holds of a half of the channels: 32 channels (16 bytes of codes) of two entries, and a
+// word of scales of some entry of its warp's.  No entry (row < 0): zeros.  The loads are volatile so that
+// they stay where they are issued, a tile ahead of their use.
 struct Piece {
     uint4 c[2];
     uint32_t s;
 };
-CSA2_D void load_piece(const Args &a, int64_t row, int chan, Piece &x) {
-    if (row >= 0) {
-        const uint8_t *p = a.kv + row * a.kv_row_stride;
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(x.c[k].x), "=r"(x.c[k].y), "=r"(x.c[k].z), "=r"(x.c[k].w) : "l"(p + chan / 2 + 16 * k));
-        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(x.s) : "l"(p + 256 + chan / 16));
-    } else {
-        x.c[0] = x.c[1] = make_uint4(0u, 0u, 0u, 0u);
-        x.s = 0u;
-    }
+CSA2_D uint4 load_codes(const Args &a, int32_t row, int byte) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (row >= 0)
+        asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(a.kv + row * a.kv_row_stride + byte));
+    return v;
 }
-// Its fp16 values as row `row` of a swizzled region.
-CSA2_D void store_piece(uint8_t *region, int row, const Piece &x) {
-    const uint32_t w[8] = {x.c[0].x, x.c[0].y, x.c[0].z, x.c[0].w, x.c[1].x, x.c[1].y, x.c[1].z, x.c[1].w};
-    const uint32_t s01 = ptx::e4m3x2_to_f16x2((uint16_t)(x.s & 0xFFFFu)), s23 = ptx::e4m3x2_to_f16x2((uint16_t)(x.s >> 16));
-    const uint32_t sc[4] = {__byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232), __byte_perm(s23, 0, 0x1010),
-                            __byte_perm(s23, 0, 0x3232)};
+CSA2_D uint32_t load_scales(const Args &a, int32_t row, int byte) {
+    uint32_t v = 0u;
+    if (row >= 0) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(a.kv + row * a.kv_row_stride + byte));
+    return v;
+}
+// 32 channels with their two scales as fp16: the 16-byte chunk at `at` of a swizzled row and the three next to it
+// (swap: the codes' second half first, so that the eight lanes of a store meet no conflicts).
+CSA2_D void store_codes(uint32_t at, bool swap, uint4 c, uint32_t scales) {
+    const uint32_t w[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
+    const uint32_t f = ptx::e4m3x2_to_f16x2((uint16_t)scales);
+    const uint32_t lo = __byte_perm(f, 0, 0x1010), hi = __byte_perm(f, 0, 0x3232);
+    const uint32_t sc[2] = {swap ? hi : lo, swap ? lo : hi};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int k = 0; k < 4; ++k) {
         uint32_t h[4];
-        ptx::e2m1x8_to_f16x8(w[i], h);
-        const uint32_t f = sc[i >> 1];
-        *reinterpret_cast<uint4 *>(region + tc::sw128_off(row, i)) =
-            make_uint4(ptx::hmul2_u32(h[0], f), ptx::hmul2_u32(h[1], f), ptx::hmul2_u32(h[2], f), ptx::hmul2_u32(h[3], f));
+        ptx::e2m1x8_to_f16x8(w[k], h);
+        const uint32_t m = sc[k >> 1];
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};"
+                     ::"r"(at ^ (k << 4)), "r"(ptx::hmul2_u32(h[0], m)), "r"(ptx::hmul2_u32(h[1], m)),
+                     "r"(ptx::hmul2_u32(h[2], m)), "r"(ptx::hmul2_u32(h[3], m)) : "memory");
     }
 }
 
@@ -664,52 +666,81 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
     }
     else {
         // ================= entries to K (first eight warps) and V (last eight) =================
-        // A thread turns 64 channels of one entry into fp16 per half.  K: entry `key` of the CTA's 64,
-        // channels 256 h + 64 (lane / 8) ..; V: entry `key` of 128, channels 64 (lane / 16) .. of the CTA's
-        // 128 of half h.  Eight neighbouring lanes have neighbouring entries: their 16-byte stores meet
-        // no conflicts in the swizzled rows.
+        // Per half a warp turns 256 channels of 8 of the CTA's 64 keys (K), or the CTA's 128 channels of 16
+        // of the 128 keys (V), into fp16.  Four neighbouring lanes have 64 contiguous bytes of codes of one
+        // entry, the next four those of the next entry: eight lanes read two lines and store without
+        // conflicts.  (One entry per lane kept the load/store pipe busy 86% of the time, more than half
+        // of that with these loads: 596 us for 128 rows x 64 heads on 32768 entries.)  The scales are read a word per
+        // lane and handed round by shuffles.
+        // (One piece of code for both operands and both halves: with a copy each the instruction cache missed.)
         const bool is_k = warp < kDeqWarp0 + kDeqWarps;
         const int dw = (warp - kDeqWarp0) & (kDeqWarps - 1);
-        const int key = is_k ? dw * 8 + (lane & 7) : dw * 16 + (lane & 15);
-        const int chan = is_k ? 64 * (lane >> 3) : 128 * rank + 64 * (lane >> 4);
-        const int off = is_k ? rank * kKeyHalf + key : key;                 // entry of the tile
+        const int keys = is_k ? 8 : 16;                                     // of the warp; lane j holds the row of key j
+        const int off = (is_k ? rank * kKeyHalf : 0) + dw * keys + (lane & (keys - 1));
+        const int region = is_k ? (lane >> 2 & 2) + (lane >> 1 & 1) : lane >> 1 & 1;
+        const int key0 = (is_k ? lane >> 4 : lane >> 3) * 2 + (lane >> 2 & 1);          // and key0 + keys / 2
+        const int code_byte = (is_k ? 0 : 64 * rank) + 32 * region + 16 * (lane & 1);
+        const int words = is_k ? 4 : 2;                                     // of scales of an entry
+        const int scale_key = is_k ? lane >> 2 : lane >> 1;
+        const int scale_byte = 256 + (is_k ? 0 : 8 * rank) + 4 * (lane & (words - 1));
+        const int from = key0 * words + region;                             // the lane with key0's scales
+        const bool swap = (lane & 2) != 0;
         const int slot = is_k ? kKSlot : kVSlot;
-        uint8_t *const dst = is_k ? sK + (lane >> 3) * kKRegion : sV + (lane >> 4) * kVRegion;
+        // keys 4 or 8 apart: the second's swizzle differs by 4 or not at all
+        const uint32_t chunk = (uint32_t)((lane & 1) * 4) ^ (swap ? 2u : 0u) ^ (uint32_t)(key0 & 7);
+        const uint32_t dst = ptx::smem_u32(is_k ? sK + region * kKRegion : sV + region * kVRegion) +
+                             (uint32_t)((dw * keys + key0) * 128) + (chunk << 4);
         uint64_t *const full = is_k ? S.k_full : S.v_full, *const empty = is_k ? S.k_empty : S.v_empty;
-        bool more = walk.next(a, sg);
-        int kt = more ? sg.k0 : 0;
-        // the cache row of this thread's entry in the next tile of the walk; -2 behind the last tile
-        auto next_row = [&]() -> int64_t {
-            if (!more) return -2;
-            const int64_t r = a.erow[(int64_t)sg.g * a.n_pad + (int64_t)kt * kTile + off];
-            if (++kt >= sg.k1) {
-                more = walk.next(a, sg);
-                kt = sg.k0;
+        int left = (int)(walk.end - walk.u);             // tiles of this pair
+        int run = 0;                                     // of the segment
+        const int32_t *rows = nullptr;                   // this thread's entry of the segment's next tile
+        // the cache row of this thread's entry in the next tile of the walk
+        auto next_row = [&]() -> int32_t {
+            if (run == 0) {
+                if (!walk.next(a, sg)) return -1;
+                run = sg.k1 - sg.k0;
+                rows = a.erow + (int64_t)sg.g * a.n_pad + (int64_t)sg.k0 * kTile + off;
             }
+            const int32_t r = *rows;
+            rows += kTile;
+            --run;
             return r;
         };
         uint32_t ph = 1;                                 // the operand's last release
-        Piece x[2];
-        int64_t row = next_row();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) load_piece(a, row, 256 * h + chan, x[h]);
-        int64_t row1 = next_row();
-        while (row != -2) {
-            const int64_t row2 = next_row();             // two tiles ahead: its load is over when it is used
-            bool bad = false;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (!ptx::mbar_wait(&empty[h], ph, abort_flag)) bad = true;
-                store_piece(dst + h * slot, key, x[h]);
-                ptx::fence_async_smem();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_rank0(&full[h]);
-                load_piece(a, row1, 256 * h + chan, x[h]);
+        Piece x, y;                                      // of this half and of the next
+        auto load = [&](Piece &p, int32_t row, int h) {
+            p.c[0] = load_codes(a, __shfl_sync(0xffffffffu, row, key0), 128 * h + code_byte);
+            p.c[1] = load_codes(a, __shfl_sync(0xffffffffu, row, key0 + keys / 2), 128 * h + code_byte);
+            p.s = load_scales(a, __shfl_sync(0xffffffffu, row, scale_key), 16 * h + scale_byte);
+        };
+        int32_t row = next_row();
+        load(x, row, 0);
+        load(y, row, 1);
+        row = next_row();
+        int32_t row1 = next_row();                       // two tiles ahead: its load is over when it is used
+#pragma unroll 1
+        for (int h = 0; left > 0;) {
+            const bool ok = ptx::mbar_wait(&empty[h], ph, abort_flag);
+            const uint32_t s0 = __shfl_sync(0xffffffffu, x.s, from);
+            const uint32_t s1 = __shfl_sync(0xffffffffu, x.s, from + keys / 2 * words);
+            const uint32_t at = dst + h * slot;
+            store_codes(at, swap, x.c[0], (lane & 1) ? s0 >> 16 : s0);
+            store_codes((at + keys / 2 * 128) ^ (is_k ? 64u : 0u), swap, x.c[1], (lane & 1) ? s1 >> 16 : s1);
+            ptx::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_rank0(&full[h]);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            load(x, row, h);
+            const Piece z = x;
+            x = y;
+            y = z;
+            h ^= 1;
+            if (h == 0) {
+                ph ^= 1;
+                --left;
+                row = row1;
+                row1 = next_row();
             }
-            if (__any_sync(0xffffffffu, bad)) break;
-            ph ^= 1;
-            row = row1;
-            row1 = row2;
         }
     }
     __syncwarp();
@@ -881,7 +912,7 @@ inline Layout layout(int rows, int H, int G, int64_t max_n) {
         return at;
     };
     l.groups = take((size_t)(G + 1) * sizeof(Group));
-    l.erow = take((size_t)G * l.n_pad * 8);
+    l.erow = take((size_t)G * l.n_pad * 4);
     l.valid = take((size_t)G * l.n_pad);
     l.qh = take((size_t)l.max_tiles * kQ * kLatent * 2);
     l.qs = take((size_t)l.max_tiles * kQ * 4);
@@ -916,7 +947,7 @@ cudaError_t launch_prefix_attn(const uint16_t *q, int rows, int H, const int32_t
     a.own_out = own_out; a.own_lse = own_lse;
     a.out = out; a.out_dtype = out_dtype; a.lse = lse;
     a.groups = reinterpret_cast<pfx::Group *>(ws + l.groups);
-    a.erow = reinterpret_cast<int64_t *>(ws + l.erow);
+    a.erow = reinterpret_cast<int32_t *>(ws + l.erow);
     a.valid = ws + l.valid;
     a.qh = reinterpret_cast<__half *>(ws + l.qh);
     a.qs = reinterpret_cast<float *>(ws + l.qs);
