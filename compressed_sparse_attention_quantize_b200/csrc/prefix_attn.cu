@@ -45,8 +45,12 @@
 // 4-11 softmax and partials; warps 12-19 entries to K, 20-27 to V (half as many, with twice the
 // channels each, took longer: their chain of wait, conversion, store and arrival was the longest).
 //
-// Bound: MMAs of N=128 take 46 cycles and N=256 60 (measured), 2432 a tile, and the tile's
-// shared-memory traffic (operands 224 KB, K and V 128 KB, P 16 KB) 2900 cycles at 128 bytes a cycle.
+// Bound: MMAs of N=128 take 46 cycles and N=256 60 (measured), 2432 a tile of about 4900; then the
+// issue slots (about half taken) and the load/store pipe (62%).  What is between is the chains of
+// waits: a half of K or V is rewritten (wait 280 cycles, conversion 700-1100, fence and arrival 150,
+// next loads) while the other half's MMAs run, and P waits for the last tile's second product.
+// 128 rows x 64 heads on 32768 entries: 569 us, 967 TFLOP/s (472 us without the entries' loads, 495
+// with half the conversions: neither alone is the bound).
 // One CTA per 64 queries with S^T = V . Q^T (N=64, one 128 KB V buffer for both products, so that the
 // softmax lay between them) took 6400 cycles a tile: 825 us for 128 rows x 64 heads on 32768 entries.
 // Every wait is bounded: on expiry the CTA records CSA2_ERR_TIMEOUT, drains, frees TMEM and exits.
@@ -113,7 +117,7 @@ struct Args {
     // workspace
     Group *groups;                         // [G + 1]
     int32_t *erow;                         // [G][n_pad]: cache rows of the entries, -1: none
-    uint8_t *valid;                        // [G][n_pad]: 1 where there is one
+    uint32_t *valid;                       // [G][n_pad / 32]: a bit for each, set where there is one
     __half *qh;                            // [tiles][128][512]
     float *qs;                             // [tiles][128]: logit per unit of S
     float *parts;                          // [pairs + tiles][2][kPartFloats]
@@ -214,13 +218,15 @@ __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(const Args a)
             } else {
                 row = a.seq_start[g] + j;
             }
-            if (row < 0 || row >= a.kv_rows) {
+            if (row < 0 || row >= a.kv_rows || row > INT32_MAX) {      // (2^31 rows are 618 GB)
                 row = -1;
                 raise_device_error(CSA2_ERR_INVALID_ARG);
             }
         }
-        a.erow[w] = row;
-        a.valid[w] = row >= 0 ? 1 : 0;
+        a.erow[w] = (int32_t)row;
+        // (a warp has 32 entries of one group, and none or all of them end here)
+        const uint32_t bits = __ballot_sync(0xffffffffu, row >= 0);
+        if (lane == 0) a.valid[w / 32] = bits;
     }
 
     // queries: a warp each, 16 channels a lane; places past a group's last query are zero
@@ -337,17 +343,16 @@ struct Piece {
     uint4 c[2];
     uint32_t s;
 };
-CSA2_D uint4 load_codes(const Args &a, int32_t row, int byte) {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (row >= 0)
-        asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(a.kv + row * a.kv_row_stride + byte));
-    return v;
+CSA2_D void load_codes(const Args &a, int32_t row, int byte, uint4 &v) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ge.s32 p, %4, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%5];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "r"(row), "l"(a.kv + row * a.kv_row_stride + byte));
 }
-CSA2_D uint32_t load_scales(const Args &a, int32_t row, int byte) {
-    uint32_t v = 0u;
-    if (row >= 0) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(a.kv + row * a.kv_row_stride + byte));
-    return v;
+CSA2_D void load_scales(const Args &a, int32_t row, int byte, uint32_t &v) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ge.s32 p, %1, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.nc.b32 %0, [%2];\n\t}"
+                 : "=&r"(v) : "r"(row), "l"(a.kv + row * a.kv_row_stride + byte));
 }
 // 32 channels with their two scales as fp16: the 16-byte chunk at `at` of a swizzled row and the three next to it
 // (swap: the codes' second half first, so that the eight lanes of a store meet no conflicts).
@@ -365,15 +370,6 @@ CSA2_D void store_codes(uint32_t at, bool swap, uint4 c, uint32_t scales) {
                      ::"r"(at ^ (k << 4)), "r"(ptx::hmul2_u32(h[0], m)), "r"(ptx::hmul2_u32(h[1], m)),
                      "r"(ptx::hmul2_u32(h[2], m)), "r"(ptx::hmul2_u32(h[3], m)) : "memory");
     }
-}
-
-// Which of 32 keys count: their 32 bytes (0 or 1) as a bit mask.
-CSA2_D uint32_t key_mask(const uint4 &a, const uint4 &b) {
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t m = 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m |= ((w[i] * 0x01020408u >> 24) & 15u) << (4 * i);
-    return m;
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -523,16 +519,13 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
         uint32_t pph = 1, sph = 0;                       // the last tile's second product; segments
         bool bad = false, aborted = false;
         while (!aborted && walk.next(a, sg)) {
-            const uint4 *valid = reinterpret_cast<const uint4 *>(a.valid + (int64_t)sg.g * a.n_pad + kh * 64 + hf * 32);
+            const uint32_t *valid = a.valid + ((int64_t)sg.g * a.n_pad >> 5) + kh * 2 + hf;
             const float zs = a.qs[sg.tile * kQ + rank * kQHalf + row];
             float mm = -INFINITY, l = 0.0f;              // running maximum - kShift; sum of the weights
-            uint4 va = valid[sg.k0 * (kTile / 16)], vb = valid[sg.k0 * (kTile / 16) + 1];
+            uint32_t next_mask = valid[sg.k0 * (kTile / 32)];
             for (int kt = sg.k0; kt < sg.k1; ++kt) {
-                const uint32_t mask = key_mask(va, vb);
-                if (kt + 1 < sg.k1) {
-                    va = valid[(kt + 1) * (kTile / 16)];
-                    vb = valid[(kt + 1) * (kTile / 16) + 1];
-                }
+                const uint32_t mask = next_mask;
+                if (kt + 1 < sg.k1) next_mask = valid[(int64_t)(kt + 1) * (kTile / 32)];
                 if (!ptx::mbar_wait(&S.s_full[sb.st], sb.ph, abort_flag)) bad = true;
                 ptx::tc_fence_after();
                 // weights under the maximum so far; a segment's first tile has none yet
@@ -670,9 +663,10 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
         // of the 128 keys (V), into fp16.  Four neighbouring lanes have 64 contiguous bytes of codes of one
         // entry, the next four those of the next entry: eight lanes read two lines and store without
         // conflicts.  (One entry per lane kept the load/store pipe busy 86% of the time, more than half
-        // of that with these loads: 596 us for 128 rows x 64 heads on 32768 entries.)  The scales are read a word per
-        // lane and handed round by shuffles.
-        // (One piece of code for both operands and both halves: with a copy each the instruction cache missed.)
+        // of that with these loads: 596 us for 128 rows x 64 heads on 32768 entries, 569 so.)  The scales
+        // are read a word per lane and handed round by shuffles.  One piece of code serves both operands
+        // and both halves, with one half's codes in registers: a copy for each missed the instruction
+        // cache (846 us), and a register more spills, to memory that has no room left in L1.
         const bool is_k = warp < kDeqWarp0 + kDeqWarps;
         const int dw = (warp - kDeqWarp0) & (kDeqWarps - 1);
         const int keys = is_k ? 8 : 16;                                     // of the warp; lane j holds the row of key j
@@ -693,33 +687,32 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
         uint64_t *const full = is_k ? S.k_full : S.v_full, *const empty = is_k ? S.k_empty : S.v_empty;
         int left = (int)(walk.end - walk.u);             // tiles of this pair
         int run = 0;                                     // of the segment
-        const int32_t *rows = nullptr;                   // this thread's entry of the segment's next tile
+        uint32_t place = 0;                              // of this thread's entry of the segment's next tile
         // the cache row of this thread's entry in the next tile of the walk
         auto next_row = [&]() -> int32_t {
             if (run == 0) {
                 if (!walk.next(a, sg)) return -1;
                 run = sg.k1 - sg.k0;
-                rows = a.erow + (int64_t)sg.g * a.n_pad + (int64_t)sg.k0 * kTile + off;
+                place = (uint32_t)((int64_t)sg.g * a.n_pad + (int64_t)sg.k0 * kTile) + off;
             }
-            const int32_t r = *rows;
-            rows += kTile;
+            const int32_t r = a.erow[place];
+            place += kTile;
             --run;
             return r;
         };
         uint32_t ph = 1;                                 // the operand's last release
-        Piece x, y;                                      // of this half and of the next
-        auto load = [&](Piece &p, int32_t row, int h) {
-            p.c[0] = load_codes(a, __shfl_sync(0xffffffffu, row, key0), 128 * h + code_byte);
-            p.c[1] = load_codes(a, __shfl_sync(0xffffffffu, row, key0 + keys / 2), 128 * h + code_byte);
-            p.s = load_scales(a, __shfl_sync(0xffffffffu, row, scale_key), 16 * h + scale_byte);
+        Piece x;                                         // of the next half: its loads run while the operand is in use
+        auto load = [&](int32_t row, int h) {
+            load_codes(a, __shfl_sync(0xffffffffu, row, key0), 128 * h + code_byte, x.c[0]);
+            load_codes(a, __shfl_sync(0xffffffffu, row, key0 + keys / 2), 128 * h + code_byte, x.c[1]);
+            load_scales(a, __shfl_sync(0xffffffffu, row, scale_key), 16 * h + scale_byte, x.s);
         };
         int32_t row = next_row();
-        load(x, row, 0);
-        load(y, row, 1);
-        row = next_row();
-        int32_t row1 = next_row();                       // two tiles ahead: its load is over when it is used
+        load(row, 0);
 #pragma unroll 1
         for (int h = 0; left > 0;) {
+            int32_t row1 = row;
+            if (h == 1) row1 = next_row();               // its load is over when it is used
             const bool ok = ptx::mbar_wait(&empty[h], ph, abort_flag);
             const uint32_t s0 = __shfl_sync(0xffffffffu, x.s, from);
             const uint32_t s1 = __shfl_sync(0xffffffffu, x.s, from + keys / 2 * words);
@@ -730,17 +723,13 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive_rank0(&full[h]);
             if (!__all_sync(0xffffffffu, ok)) break;
-            load(x, row, h);
-            const Piece z = x;
-            x = y;
-            y = z;
+            row = row1;
             h ^= 1;
             if (h == 0) {
                 ph ^= 1;
                 --left;
-                row = row1;
-                row1 = next_row();
             }
+            load(row, h);
         }
     }
     __syncwarp();
@@ -913,7 +902,7 @@ inline Layout layout(int rows, int H, int G, int64_t max_n) {
     };
     l.groups = take((size_t)(G + 1) * sizeof(Group));
     l.erow = take((size_t)G * l.n_pad * 4);
-    l.valid = take((size_t)G * l.n_pad);
+    l.valid = take((size_t)G * l.n_pad / 8);
     l.qh = take((size_t)l.max_tiles * kQ * kLatent * 2);
     l.qs = take((size_t)l.max_tiles * kQ * 4);
     l.parts = take((size_t)(l.pairs + l.max_tiles) * 2 * kPartFloats * 4);
@@ -948,7 +937,7 @@ cudaError_t launch_prefix_attn(const uint16_t *q, int rows, int H, const int32_t
     a.out = out; a.out_dtype = out_dtype; a.lse = lse;
     a.groups = reinterpret_cast<pfx::Group *>(ws + l.groups);
     a.erow = reinterpret_cast<int32_t *>(ws + l.erow);
-    a.valid = ws + l.valid;
+    a.valid = reinterpret_cast<uint32_t *>(ws + l.valid);
     a.qh = reinterpret_cast<__half *>(ws + l.qh);
     a.qs = reinterpret_cast<float *>(ws + l.qs);
     a.parts = reinterpret_cast<float *>(ws + l.parts);

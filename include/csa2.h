@@ -595,8 +595,9 @@ CSA2_API csa2_status csa2_page_ids(const int32_t *ids, int B, int T, int K, cons
  *   for the product with the exact fp16 entries.
  * Limits: D == 512; H a multiple of 16, 16 <= H <= CSA2_MAX_HEADS; 1 <= G <= CSA2_MAX_PREFIX_GROUPS;
  *   q, kv, kv_row_stride, own_out and out 16-byte aligned.
- * Workspace: csa2_prefix_attn_workspace_size(rows, H, G, max_n, &bytes): the prefixes in fp16 (1 KB
- *   per entry of G * max_n), the queries (1 KB per head), partials (128 KB per 64 queries and SM).
+ * Workspace: csa2_prefix_attn_workspace_size(rows, H, G, max_n, &bytes): the entries' cache rows (about 4
+ *   bytes per entry of G * max_n), the queries in fp16 (1 KB per head, each group's padded to 128
+ *   heads) and fp32 partials (257 KB per 128 heads and per pair of SMs).
  *   Calls that may overlap (other streams, two graphs) need workspaces of their own.
  * Errors: INVALID_ARG (NULL q, row_start, kv, n_prefix, out, or both table and seq_start; one of own_out
  *   and own_lse without the other; unknown out_dtype), SHAPE (rows < 1 or rows * H > 2^24, H, G, max_n < 0
