@@ -353,6 +353,7 @@ def test_prefix_refusals():
         assert call(**{k: 18}) == ALIGN, k
     assert call(ws=None) == WS and call(wb=1000) == WS
     size = csa2.csa2_prefix_attn_workspace_size(32, 64, 1, 32768)
-    assert size > 32768 * 1024
+    assert size >= 32 * 64 * 1024 + 4 * 32768                     # queries in fp16, the entries' cache rows
+    assert size < csa2.csa2_prefix_attn_workspace_size(32, 64, 1, 1 << 22)
     with pytest.raises(csa2.CSA2Error, match="SHAPE"):
         csa2.csa2_prefix_attn_workspace_size(32, 60, 1, 32768)
