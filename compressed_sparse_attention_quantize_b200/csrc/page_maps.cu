@@ -14,7 +14,13 @@
 // shared memory.  No CTA reads what another writes: a new entry's page comes from the free list
 // itself, not from the table, and the list's position is read from one word and written to another.
 // Bound: the maps' bytes (12 per token place, 8 per entry place) for long prefill steps, launch
-// latency for a decode step.
+// latency for a decode step.  Measured (in a graph): 32 decode requests 5.6 us; 256 prefill chunks (29 MB of
+// maps) 12.2 us, of which the scans about 4; with 64-bit divisions and lengths read again from
+// global memory in the search 16.3.
+//
+// page_ids_kernel: an id is a division, a table look-up in shared memory and a store.  Bound by
+// memory: 4096 rows of 2048 ids 15.6 us in a graph, 4.3 TB/s; with a division instruction per id and the table
+// in global memory 19.1.
 #include <algorithm>
 
 #include "common.cuh"
