@@ -368,7 +368,8 @@ csa2_status csa2_page_maps(const int32_t *old_tokens, const int32_t *new_tokens,
         window > (1 << 20) || max_pages < 1 || n_free < 0 || cap_entries < 0 || cap_tokens < 0)
         return CSA2_ERR_SHAPE;
     if (!old_tokens || !new_tokens || !table || (!free_pages && n_free > 0) || !free_next || !free_next_out ||
-        free_next == free_next_out || !n_entries || !entry_off || (!entry_rows && cap_entries > 0) || !token_off)
+        free_next == free_next_out || n_entries == old_tokens || n_entries == new_tokens ||
+        (swa_len && (swa_len == old_tokens || swa_len == new_tokens || swa_len == n_entries)) || !n_entries || !entry_off || (!entry_rows && cap_entries > 0) || !token_off)
         return CSA2_ERR_INVALID_ARG;
     if (!aligned_to(old_tokens, 4) || !aligned_to(new_tokens, 4) || !aligned_to(table, 4) || !aligned_to(free_pages, 4) ||
         !aligned_to(free_next, 4) || !aligned_to(free_next_out, 4) || !aligned_to(n_entries, 4) ||

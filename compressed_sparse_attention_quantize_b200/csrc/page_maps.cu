@@ -371,9 +371,9 @@ cudaError_t launch_page_ids(const int32_t *ids, int64_t rows, int T, int K, cons
     while (B * ceil_div(T, chunk) > INT32_MAX) chunk *= 2;
     a.chunk = (int)chunk;
     a.chunks = (int)ceil_div(T, chunk);
-    const int bytes = max_pages * 4;
     a.staged = max_pages <= 12288 && chunk * K * 2 >= max_pages;
-    pm::page_ids_kernel<<<(unsigned)(B * a.chunks), pm::kThreads, a.staged ? bytes : 0, st>>>(a);
+    const int bytes = a.staged ? max_pages * 4 : 0;
+    pm::page_ids_kernel<<<(unsigned)(B * a.chunks), pm::kThreads, bytes, st>>>(a);
     note_launches(1);
     return cudaGetLastError();
 }

@@ -541,6 +541,8 @@ CSA2_API csa2_status csa2_fp4_matmul(int fmt, const uint8_t *a_codes, int64_t a_
  *   table width that does not suffice (the missing pages are -1, their rows -1, n_entries counts
  *   the entries that have a page) and more new tokens or entries than the maps hold record
  *   CSA2_ERR_SHAPE in the device error word.
+ *   Every CTA reads the lengths, so no output may share memory with an input or another output
+ *   (n_entries or swa_len given as a length array are refused: INVALID_ARG).
  * Errors: INVALID_ARG (a NULL array other than those marked; entry_rows may be NULL when
  *   cap_entries is 0 and free_pages when n_free is 0), SHAPE (B < 1 or > CSA2_MAX_REQUESTS, ratio,
  *   page_entries, window or max_pages < 1, page_entries or window > 2^20, n_free, cap_entries or

@@ -219,3 +219,56 @@ def test_matmul_refusals():
     assert csa2.csa2_fp4_matmul_workspace_size(1, 1, 16) > 0
     with pytest.raises(csa2.CSA2Error, match="SHAPE"):
         csa2.csa2_fp4_matmul_workspace_size(1, 1, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [csa2.FMT_FP4, csa2.FMT_MXFP4])
+@pytest.mark.parametrize("M,N,K", [(3, 200, 1600), (300, 333, 1120), (1200, 3100, 1600)])
+def test_matmul_padding_is_not_read(M, N, K, fmt):
+    """Code and scale rows that end inside an aligned 16 bytes, with NaN scales and codes behind their ends."""
+    blk = block_of(fmt)
+    nb = K // blk
+    g = torch.Generator().manual_seed(4)
+    ops = []
+    for rows in (M, N):
+        c, s = operand(g, rows, K, fmt, code_pad=16, scale_pad=-nb % 16 + 16)
+        assert s.stride(0) % 16 == 0
+        c[:, K // 2:] = 0x77
+        s[:, nb:] = 0x7F if fmt == csa2.FMT_FP4 else 0xFF
+        ops += [c, s]
+    a, sa, b, sb = ops
+    out = torch.empty(M, N, device="cuda")
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    csa2.csa2_fp4_matmul(fmt, a, a.stride(0), sa, sa.stride(0), b, b.stride(0), sb, sb.stride(0), M, N, K, 1.0, out, 0, N,
+                         ws, 256)
+    va, vb = values(a[:, :K // 2], sa[:, :nb].contiguous(), fmt), values(b[:, :K // 2], sb[:, :nb].contiguous(), fmt)
+    tol = (K / 16 + 66) * 2.0 ** -23 * (va.abs() @ vb.abs().t())
+    assert ((out.double() - va @ vb.t()).abs() <= tol).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [csa2.FMT_FP4, csa2.FMT_MXFP4])
+def test_linear_far_rows(fmt):
+    """Inputs and outputs beyond 2^31 elements: rows there equal the same rows near the start."""
+    M, N, K = 70001, 32776, 64
+    blk = block_of(fmt)
+    g = torch.Generator().manual_seed(6)
+    b, sb = operand(g, N, K, fmt)
+    x = torch.randn(40, K, generator=g).bfloat16().cuda()
+    wide = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    wide[:40, :K], wide[M - 40:, :K] = x, x
+    codes = torch.zeros(M, 32, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(M, K // blk, dtype=torch.uint8, device="cuda")
+    csa2.csa2_quantize_kv(fmt, wide[M - 40:], csa2.DTYPE_BF16, 40, K, N, codes[M - 40:], 32, scales[M - 40:], K // blk)
+    whole, whole_s = torch.zeros_like(codes), torch.zeros_like(scales)
+    csa2.csa2_quantize_kv(fmt, wide, csa2.DTYPE_BF16, M, K, N, whole, 32, whole_s, K // blk)
+    assert torch.equal(whole[M - 40:], codes[M - 40:]) and torch.equal(whole_s[M - 40:], scales[M - 40:])
+    codes[:40], scales[:40] = codes[M - 40:], scales[M - 40:]
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    csa2.csa2_fp4_matmul(fmt, codes, 32, scales, K // blk, b, b.stride(0), sb, sb.stride(0), M, N, K, 1.0, wide,
+                         csa2.DTYPE_BF16, N, ws, 256)
+    va, vb = values(codes[:40], scales[:40], fmt), values(b[:, :K // 2], sb, fmt)
+    ref, mag = va @ vb.t(), va.abs() @ vb.abs().t()
+    assert torch.equal(wide[:40], wide[M - 40:])
+    assert ((wide[:40].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (K / 16 + 10) * 2.0 ** -23 * mag).all()
+    assert csa2.csa2_device_error() == 0

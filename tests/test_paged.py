@@ -277,7 +277,7 @@ def test_maps_refusals(L):
     names = ("old", "new", "B", "ratio", "E", "window", "table", "max_pages", "free", "n_free", "next", "next_out",
              "n_entries", "swa_len", "entry_off", "entry_rows", "cap_entries", "token_off", "window_rows", "q_pos",
              "cap_tokens", "stream")
-    good = dict(zip(names, (16, 16, 4, 4, 64, 128, 16, 8, 16, 8, 16, 32, 16, 16, 16, 16, 9, 16, 16, 16, 9, None)))
+    good = dict(zip(names, (16, 16, 4, 4, 64, 128, 16, 8, 16, 8, 16, 32, 48, 64, 16, 16, 9, 16, 16, 16, 9, None)))
 
     def call(**kw):
         a = {**good, **kw}
@@ -291,6 +291,7 @@ def test_maps_refusals(L):
     for k in ("old", "new", "table", "free", "next", "next_out", "n_entries", "entry_off", "entry_rows", "token_off"):
         assert call(**{k: None}) == INVALID
     assert call(next_out=16) == INVALID                     # the position's two words are one
+    assert call(n_entries=16) == INVALID and call(swa_len=16) == INVALID and call(swa_len=48) == INVALID
     for k in ("old", "new", "table", "free", "next", "next_out", "n_entries", "swa_len", "q_pos"):
         assert call(**{k: 18}) == ALIGN
     for k in ("entry_off", "entry_rows", "token_off", "window_rows"):

@@ -357,3 +357,23 @@ def test_prefix_refusals():
     assert size < csa2.csa2_prefix_attn_workspace_size(32, 64, 1, 1 << 22)
     with pytest.raises(csa2.CSA2Error, match="SHAPE"):
         csa2.csa2_prefix_attn_workspace_size(32, 60, 1, 32768)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("paged", [False, True])
+def test_far_rows(paged):
+    """Entries more than 2^32 bytes into the cache: what the same entries give near its start."""
+    near = Case([260, 100], [0, 2, 5], 5, 16, page=16 if paged else None, seed=21)
+    near.run()
+    out, lse = near.out.clone(), near.lse.clone()
+    shift = 16 * 1000000                                       # rows, whole pages
+    kv = torch.empty((shift + near.kv_rows, near.stride), dtype=torch.uint8, device="cuda")
+    kv[shift:] = near.kv
+    near.kv, near.kv_rows = kv, kv.shape[0]
+    if paged:
+        near.table = torch.where(near.table >= 0, near.table + shift // 16, near.table)
+    else:
+        near.seq = near.seq + shift
+    near.run()
+    assert csa2.csa2_device_error() == 0
+    assert torch.equal(out, near.out) and torch.equal(lse, near.lse)

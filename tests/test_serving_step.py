@@ -200,3 +200,26 @@ def test_serving_steps(graph):
         assert np.array_equal(s.table.cpu().numpy(), table) and s.next.tolist()[1] == nxt
         assert np.array_equal(s.er.cpu().numpy(), ref["entry_rows"]) and np.array_equal(s.wr.cpu().numpy(), ref["window_rows"])
         s.check(old, new, latents, tokens)
+
+
+def test_two_steps_at_once():
+    """Two programs with buffers and workspaces of their own on two streams: bit for bit what each gives alone."""
+    def fresh(seed):
+        s = Step(seed)
+        s.begin(*STEPS[0], 20 + seed)
+        return s
+    alone = [fresh(1), fresh(2)]
+    for s in alone:
+        s.run()
+        torch.cuda.synchronize()
+    both, streams = [fresh(1), fresh(2)], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):                                      # the same step again: it writes the same bytes
+        for s, st in zip(both, streams):
+            with torch.cuda.stream(st):
+                s.run()
+    torch.cuda.synchronize()
+    assert csa2.csa2_device_error() == 0
+    for a, b in zip(alone, both):
+        for name in ("q", "latent", "own", "own_lse", "out", "lse", "kv", "win", "er", "wr", "table"):
+            assert torch.equal(getattr(a, name).view(torch.uint8), getattr(b, name).view(torch.uint8)), name
