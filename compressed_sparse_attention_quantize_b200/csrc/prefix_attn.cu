@@ -633,8 +633,10 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
             // store 64 bytes of a row together
             float *dst = part + 2 * kQHalf + 256 * hf + 128 * kh + 4 * (lane & 3);
             const int r0 = (sub & 1) * 32;               // the warp's first query
+            const Group &gr = a.groups[sg.g];            // queries of the CTA's 64 that there are
+            const int there = (int)min((int64_t)kQHalf, (int64_t)gr.rows * a.H - (sg.tile - gr.tile0) * kQ - rank * kQHalf);
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 16) {
+            for (int c = 0; r0 < there && c < 128; c += 16) {
                 uint32_t o[16];
                 ptx::tmem_ld16(lane_addr + kOCol + 128 * hf + c, o);
                 ptx::tmem_ld_wait();
@@ -646,8 +648,9 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int r = r0 + 8 * k + (lane >> 2);
-                    *reinterpret_cast<uint4 *>(dst + r * kLatent + c) =
-                        *reinterpret_cast<const uint4 *>(p_row + tc::sw128_off(r, hf * 4 + (lane & 3)));
+                    if (r < there)
+                        *reinterpret_cast<uint4 *>(dst + r * kLatent + c) =
+                            *reinterpret_cast<const uint4 *>(p_row + tc::sw128_off(r, hf * 4 + (lane & 3)));
                 }
                 __syncwarp();
             }
