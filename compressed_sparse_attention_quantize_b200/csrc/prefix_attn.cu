@@ -336,6 +336,16 @@ CSA2_D uint32_t desc_low(const void *p, uint32_t lbo_bytes) {
     return (uint32_t)ptx::sdesc_sw128(ptx::smem_u32(p), lbo_bytes, 1024);
 }
 
+// 32 columns of 16 TMEM lanes: word 4 k + j of thread t is column 8 k + 2 (t % 4) + j % 2 of lane
+// t / 4 + 8 (j / 2).
+CSA2_D void tmem_ld_rows16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
 // What a thread holds of a half of the channels: 32 channels (16 bytes of codes) of two entries, and a
 // word of scales of some entry of its warp's.  No entry (row < 0): zeros.  The loads are volatile so that
 // they stay where they are issued, a tile ahead of their use.
@@ -559,10 +569,10 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
                         add += sum[0] + sum[1];
                     }
                 };
-                weights();
-                float al = 1.0f;
                 // one barrier decides whether to stop and whether some maximum moves
-                if (tc::block_any(over || bad || *abort_flag != 0, bar, 128)) {
+                if (kt > sg.k0) weights();
+                float al = 1.0f;
+                if (kt == sg.k0 || tc::block_any(over || bad || *abort_flag != 0, bar, 128)) {
                     if (tc::block_any(bad || *abort_flag != 0, bar, 128)) { aborted = true; break; }
                     float top = -INFINITY;
 #pragma unroll 1
@@ -629,31 +639,27 @@ prefix_attn_kernel(const Args a, const __grid_constant__ CUtensorMap qmap) {
                 part[row] = mm;
                 part[kQHalf + row] = (S.red[0][row] + S.red[1][row]) + (S.red[2][row] + S.red[3][row]);
             }
-            // 16 columns at a time through this warp's own bytes of P (at rest now), so that four lanes
-            // store 64 bytes of a row together
-            float *dst = part + 2 * kQHalf + 256 * hf + 128 * kh + 4 * (lane & 3);
-            const int r0 = (sub & 1) * 32;               // the warp's first query
+            // four lanes hold 8 columns of a row and store them together, a whole sector
             const Group &gr = a.groups[sg.g];            // queries of the CTA's 64 that there are
             const int there = (int)min((int64_t)kQHalf, (int64_t)gr.rows * a.H - (sg.tile - gr.tile0) * kQ - rank * kQHalf);
+            const int r0 = (sub & 1) * 32;               // the warp's first query
+            const int o0 = 2 * kQHalf + (r0 + (lane >> 2)) * kLatent + 256 * hf + 128 * kh + 2 * (lane & 3);
 #pragma unroll 1
-            for (int c = 0; r0 < there && c < 128; c += 16) {
-                uint32_t o[16];
-                ptx::tmem_ld16(lane_addr + kOCol + 128 * hf + c, o);
-                ptx::tmem_ld_wait();
+            for (int i = r0; i < min(there, r0 + 32); i += 16)
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t o[16];
+                    tmem_ld_rows16(lane_addr + ((uint32_t)(i - r0) << 16) + kOCol + 128 * hf + c, o);
+                    ptx::tmem_ld_wait();
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    *reinterpret_cast<uint4 *>(p_row + tc::sw128_off(row, hf * 4 + q)) =
-                        make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-                __syncwarp();
+                    for (int g = 0; g < 2; ++g)
+                        if (i + 8 * g + (lane >> 2) < there) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int r = r0 + 8 * k + (lane >> 2);
-                    if (r < there)
-                        *reinterpret_cast<uint4 *>(dst + r * kLatent + c) =
-                            *reinterpret_cast<const uint4 *>(p_row + tc::sw128_off(r, hf * 4 + (lane & 3)));
+                            for (int k = 0; k < 4; ++k)
+                                *reinterpret_cast<uint2 *>(part + (o0 + (i - r0 + 8 * g) * kLatent + c + 8 * k)) =
+                                    make_uint2(o[4 * k + 2 * g], o[4 * k + 2 * g + 1]);
+                        }
                 }
-                __syncwarp();
-            }
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive_rank0(&S.o_free);
