@@ -31,11 +31,14 @@
 // tile in its shared memory, and every CTA adds up a share of the columns over the cluster in rank
 // order (no second launch, no atomics: the result does not depend on timing).
 //
-// Bound of large products: shared memory at 128 bytes a cycle.  A CTA of 128 x 192 writes and reads
-// 40 KB of codes a stage, writes 6 and reads 24 KB of scales (every lane quarter of TMEM needs them
-// all): 880 cycles for 192 columns (1006 measured, 87 us for 4096 x 8192 x 4096 with E4M3 scales); one of
-// a pair 32 KB of codes and 30 of scales, 750 for 256 columns (65 us, 4.2 PFLOP/s, of which the MMAs'
-// wait for the epilogue is 8; sustained, the power limit makes it 75).  Decode batches: the weights' bytes.
+// Bound of large products: the scales' way.  A buffer of them in TMEM is free when the stage's MMAs have
+// completed, and is read again a wait, a read of shared memory, tcgen05.st and an arrival later; with the two
+// buffers that 192 columns leave, a stage takes 1000 cycles for 384 of MMAs (87 us for 4096 x 8192 x
+// 4096 with E4M3 scales; the same by pairs of CTAs on 256 x 192 with two accumulators, 86 us).  With
+// four, beside one accumulator of 256 columns, it takes 800 for 512 and a tile 2500 more while the
+// epilogue reads it: 65 us, 4.2 PFLOP/s (8 of it the epilogue; sustained, the power limit makes it 75).
+// Shared memory moves 62 KB a stage of a pair's CTA, about 500 cycles.  Decode batches: the weights'
+// bytes (32 x 32768 x 4096: 18.6 us in a graph beside the quantiser, 1.73 waves of tiles).
 // Every wait is bounded: on expiry the CTA records CSA2_ERR_TIMEOUT, drains, frees TMEM and exits.
 #include "common.cuh"
 #include "tc_ptx.cuh"

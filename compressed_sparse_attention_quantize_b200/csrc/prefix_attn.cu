@@ -46,11 +46,12 @@
 // channels each, took longer: their chain of wait, conversion, store and arrival was the longest).
 //
 // Bound: MMAs of N=128 take 46 cycles and N=256 60 (measured), 2432 a tile of about 4900; then the
-// issue slots (about half taken) and the load/store pipe (62%).  What is between is the chains of
+// issue slots (about half taken) and the load/store pipe (59%).  What is between is the chains of
 // waits: a half of K or V is rewritten (wait 280 cycles, conversion 700-1100, fence and arrival 150,
 // next loads) while the other half's MMAs run, and P waits for the last tile's second product.
-// 128 rows x 64 heads on 32768 entries: 569 us, 967 TFLOP/s (472 us without the entries' loads, 495
-// with half the conversions: neither alone is the bound).
+// 128 rows x 64 heads on 32768 entries: 562 us, 978 TFLOP/s (472 us without the entries' loads, 495
+// with half the conversions: neither alone is the bound).  One row of 16 heads on 1000 entries: 17.5 us in a
+// graph, of which this launch is about 11 (partials of absent queries are not stored: 21.2 with them).
 // One CTA per 64 queries with S^T = V . Q^T (N=64, one 128 KB V buffer for both products, so that the
 // softmax lay between them) took 6400 cycles a tile: 825 us for 128 rows x 64 heads on 32768 entries.
 // Every wait is bounded: on expiry the CTA records CSA2_ERR_TIMEOUT, drains, frees TMEM and exits.
