@@ -192,11 +192,13 @@ def _ptr(x) -> Optional[int]:
     """Device address of a tensor (or an int address, or None)."""
     if x is None:
         return None
-    if isinstance(x, int):
-        return x
-    if not getattr(x, "is_cuda", False):
-        raise CSA2Error("expected a CUDA tensor or a device address")
-    return x.data_ptr()
+    try:                                                   # tensors first: a call has up to 15 of them
+        if x.is_cuda:
+            return x.data_ptr()
+    except AttributeError:
+        if isinstance(x, int):
+            return x
+    raise CSA2Error("expected a CUDA tensor or a device address")
 
 
 _current_raw_stream = None
