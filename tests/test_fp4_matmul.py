@@ -272,3 +272,32 @@ def test_linear_far_rows(fmt):
     assert torch.equal(wide[:40], wide[M - 40:])
     assert ((wide[:40].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (K / 16 + 10) * 2.0 ** -23 * mag).all()
     assert csa2.csa2_device_error() == 0
+
+
+@pytest.mark.gpu
+def test_matmul_after_copies_in_a_graph():
+    """A captured product that follows memory copies, one of them on a joined stream, reads what they wrote."""
+    M, N, K, fmt = 70, 600, 512, csa2.FMT_MXFP4
+    g = torch.Generator().manual_seed(8)
+    (a, sa), (b, sb) = operand(g, M, K, fmt), operand(g, N, K, fmt)
+    a1, b1 = torch.zeros_like(a), torch.zeros_like(b)
+    out = torch.empty(M, N, device="cuda")
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    side, other, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        other.wait_stream(side)
+        with torch.cuda.stream(other):
+            b1.copy_(b)
+        a1.copy_(a)
+        side.wait_stream(other)
+        csa2.csa2_fp4_matmul(fmt, a1, K // 2, sa, K // 32, b1, K // 2, sb, K // 32, M, N, K, 1.0, out, 0, N, ws, 256)
+        a1.zero_()                                          # after the product has read it
+    for _ in range(3):
+        out.fill_(-1.0)
+        a.random_(0, 256)
+        graph.replay()
+        torch.cuda.synchronize()
+        va, vb = values(a, sa, fmt), values(b, sb, fmt)
+        tol = (K / 16 + 66) * 2.0 ** -23 * (va.abs() @ vb.abs().t())
+        assert ((out.double() - va @ vb.t()).abs() <= tol).all()
